@@ -1,0 +1,260 @@
+// Shared by the matrix-product kernels: the scaled matrix instruction, E8M0
+// helpers, expert shards and the output epilogue.
+//
+// v_mfma_scale_f32_16x16x128_f8f6f4 computes D[i][j] += sum_k A[i][k] 2^(sa-127)
+// B[j][k] 2^(sb-127) over 128 values of k.  Lane l holds, of either operand,
+// row l % 16 and the 32 consecutive k from 32 g, g = l / 16 -- 16 bytes of E2M1
+// codes, one MX block, so each lane supplies the E8M0 byte of its own block.
+// D's lane l holds column l % 16 and rows 4 g .. 4 g + 3.
+// The weights are operand A throughout, so a lane ends with four consecutive
+// output columns of one token and stores them as one vector.
+#pragma once
+
+#include <type_traits>
+
+#include "device_common.hpp"
+
+namespace fp4mi {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kE2M1 = 4;   // the instruction's operand format field
+
+// The 16 or 32 bytes one lane holds of an operand.
+template <bool F8>
+struct Frag {
+  i32x4 lo;
+};
+template <>
+struct Frag<true> {
+  i32x4 lo, hi;
+};
+
+// SA, SB: which byte of the scale words sa, sb this instruction uses.
+template <int SA, int SB>
+__device__ __forceinline__ f32x4 mfma_scaled(const Frag<false>& a, const Frag<false>& b, f32x4 c,
+                                             int sa, int sb) {
+  const i32x8 x = {a.lo.x, a.lo.y, a.lo.z, a.lo.w, 0, 0, 0, 0};
+  const i32x8 y = {b.lo.x, b.lo.y, b.lo.z, b.lo.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, kE2M1, kE2M1, SA, sa, SB, sb);
+}
+
+// Products with an FP8 operand.  The scaled instruction lines the products of
+// adjacent k up with the largest of them and drops what lies 14 bits or more
+// below it; over E4M3's 18 binades that costs about 2e-5 of a sum (measured on
+// Gaussian rows), which is not a sum in fp32.  E2M1 by E2M1 spans 8 bits and
+// loses nothing, but E4M3 goes through bf16 products, which are exact and are
+// added in fp32 (6e-8 measured), at half the scaled instruction's rate.  A
+// lane then holds the 32 consecutive k from 32 g of both operands, and
+// instruction q of four takes its 8 from 8 q.
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ bf16x8_t join(bf16x2_t a, bf16x2_t b, bf16x2_t c, bf16x2_t d) {
+  return bf16x8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+template <int Q>
+__device__ __forceinline__ bf16x8_t bf16_of(const Frag<false>& f, float scale) {
+  const uint32_t w = (uint32_t)f.lo[Q];
+  return join(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0),
+              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1),
+              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2),
+              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
+}
+template <int Q>
+__device__ __forceinline__ bf16x8_t bf16_of(const Frag<true>& f, float scale) {
+  const uint32_t a = (uint32_t)(Q < 2 ? f.lo[(2 * Q) & 3] : f.hi[(2 * Q) & 3]);
+  const uint32_t b = (uint32_t)(Q < 2 ? f.lo[(2 * Q + 1) & 3] : f.hi[(2 * Q + 1) & 3]);
+  return join(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false),
+              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, true),
+              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, false),
+              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, true));
+}
+// 2^(byte - 127) as the converters' scale operand.
+__device__ __forceinline__ float scale_of(int byte) { return __uint_as_float((uint32_t)byte << 23); }
+
+// Scales 2^-100 .. 2^100: code times scale is then a normal bf16 value.
+__device__ __forceinline__ bool scale_in_window(int byte) { return (unsigned)(byte - 27) <= 200u; }
+// So does any scale but NaN over codes that are all zero (a block of zeros has
+// byte 0).
+__device__ __forceinline__ bool zero_codes(const Frag<false>& f) {
+  return ((f.lo.x | f.lo.y | f.lo.z | f.lo.w) & 0x77777777) == 0;
+}
+__device__ __forceinline__ bool zero_codes(const Frag<true>& f) {
+  return ((f.lo.x | f.lo.y | f.lo.z | f.lo.w | f.hi.x | f.hi.y | f.hi.z | f.hi.w) & 0x7F7F7F7F) == 0;
+}
+template <typename L>
+__device__ __forceinline__ bool scale_fits(const L& f) {
+  return scale_in_window(f.s) || (f.s < 228 && zero_codes(f.v));
+}
+
+// The four instructions of a step, with scale(i) for row fragment i.
+template <int N, int M, typename LA, typename LB, typename SA, typename SB>
+__device__ __forceinline__ void bf16_quarters(const LA (&a)[N], const LB (&b)[M], SA sa, SB sb,
+                                              f32x4 (&acc)[N][M]) {
+  auto quarter = [&](auto q) {
+    bf16x8_t x[N], y[M];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = bf16_of<decltype(q)::value>(a[i].v, sa(i));
+#pragma unroll
+    for (int j = 0; j < M; ++j) y[j] = bf16_of<decltype(q)::value>(b[j].v, sb(j));
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < M; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+  };
+  quarter(std::integral_constant<int, 0>());
+  quarter(std::integral_constant<int, 1>());
+  quarter(std::integral_constant<int, 2>());
+  quarter(std::integral_constant<int, 3>());
+}
+
+// 16 x 16 x 128 of the above: N row fragments of A by M of B, fragments with
+// their scale byte (.v, .s).  If any lane's scale is outside the window (a NaN
+// scale included), the step's four blocks of 32 run one by one on the bare
+// codes, and the two scales multiply each block's sum in fp32.
+template <int N, int M, typename LA, typename LB>
+__device__ __forceinline__ void mfma_bf16_step(const LA (&a)[N], const LB (&b)[M], f32x4 (&acc)[N][M]) {
+  bool fine = true;
+#pragma unroll
+  for (int i = 0; i < N; ++i) fine &= scale_in_window(a[i].s);
+#pragma unroll
+  for (int j = 0; j < M; ++j) fine &= scale_in_window(b[j].s);
+  if (!__all(fine)) {
+    fine = true;
+#pragma unroll
+    for (int i = 0; i < N; ++i) fine &= scale_fits(a[i]);
+#pragma unroll
+    for (int j = 0; j < M; ++j) fine &= scale_fits(b[j]);
+  }
+  if (__all(fine)) {
+    bf16_quarters(a, b, [&](int i) { return scale_of(a[i].s); },
+                  [&](int j) { return scale_of(b[j].s); }, acc);
+    return;
+  }
+  const int g = (threadIdx.x & 63) >> 4, r = threadIdx.x & 15;
+#pragma unroll 1
+  for (int blk = 0; blk < 4; ++blk) {
+    LA one[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      one[i] = a[i];
+      if (g != blk) one[i].v = {};
+    }
+    f32x4 part[N][M] = {};
+    bf16_quarters(one, b, [](int) { return 1.0f; }, [](int) { return 1.0f; }, part);
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const int sb = __shfl(b[j].s, 16 * blk + r);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int sa = __shfl(a[i].s, 16 * blk + 4 * g + c);
+          acc[i][j][c] += (sa == 255 || sb == 255) ? __builtin_nanf("")
+                                                   : ldexpf(part[i][j][c], sa + sb - 254);
+        }
+    }
+  }
+}
+
+// A power-of-two fp32 scale as its E8M0 byte (2^-127, an fp32 subnormal, is
+// byte 0); sign and fraction bits are not read.
+__device__ __forceinline__ uint32_t e8m0_of(float s) {
+  return (__float_as_uint(s) >> 23) & 0xFFu;
+}
+
+// Operands of C[t, :] = A[t, :] . W[e]^T, rows t of shard e.  offsets is
+// null for a plain product (one shard of `tokens` rows).
+struct ProductArgs {
+  const uint8_t* a;          // MXFP4 [T, K/2] or E4M3 [T, K]
+  const void* a_scales;      // UE8M0 [T, K/32] or fp32 [T, K/128]
+  const float* a_row_scale;  // fp32 [T] or null
+  const uint8_t* w;          // [E, N, K/2]
+  const uint8_t* w_scales;   // [E, N, K/32]
+  const int64_t* offsets;    // [E + 1] or null
+  void* out;                 // [T, N]
+  int64_t tokens;
+  int experts;
+  int n, k;
+  int n_tiles;               // tiles along N
+};
+
+// Rows [lo, hi) of `tokens` that shard e owns; malformed offsets are clamped,
+// so that whatever they hold every access stays inside the buffers.
+__device__ __forceinline__ void shard_bounds(const int64_t* off, int e, int tokens, int& lo,
+                                             int& hi) {
+  const int64_t a = off[e], b = off[e + 1];
+  lo = (int)(a < 0 ? 0 : (a > tokens ? tokens : a));
+  hi = (int)(b < lo ? lo : (b > tokens ? tokens : b));
+}
+
+// The shard and first row of row tile `mt`, tiles counted shard by shard with
+// ceil(n_e / BM) each.  A wave looks at 64 shards at a time: each lane counts
+// its shard's tiles and a prefix sum finds the one that holds mt.  False past
+// the last tile.  The result is the same in every lane.
+template <int BM>
+__device__ __forceinline__ bool locate_tile(const int64_t* off, int experts, int tokens, int mt,
+                                            int& e, int& row0, int& row_end) {
+  const int lane = threadIdx.x & 63;
+  int base = 0;
+  for (int e0 = 0; e0 < experts; e0 += 64) {
+    int lo = 0, hi = 0;
+    if (e0 + lane < experts) shard_bounds(off, e0 + lane, tokens, lo, hi);
+    const int own = (hi - lo + BM - 1) / BM;
+    int sum = own;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(sum, d);
+      if (lane >= d) sum += v;
+    }
+    const int total = __builtin_amdgcn_readlane(sum, 63);
+    if (mt < base + total) {
+      const int src = __builtin_ctzll(__ballot(base + sum > mt));
+      const int before = base + __builtin_amdgcn_readlane(sum, src) - __builtin_amdgcn_readlane(own, src);
+      e = e0 + src;
+      row0 = __builtin_amdgcn_readlane(lo, src) + (mt - before) * BM;
+      row_end = __builtin_amdgcn_readlane(hi, src);
+      return true;
+    }
+    base += total;
+  }
+  return false;
+}
+
+// Row tiles of at most this many exist: sum ceil(n_e / bm) over non-empty shards.
+inline int64_t max_row_tiles(int64_t tokens, int64_t experts, int bm, bool grouped) {
+  return grouped ? tokens / bm + (experts < tokens ? experts : tokens) : (tokens + bm - 1) / bm;
+}
+
+// Four consecutive columns n .. n+3 of one output row, rounded once to the
+// output type (fp32 sums to here); columns past the row's end are dropped.
+template <bool BF16>
+__device__ __forceinline__ void store_out4(void* out, int64_t row, int n_cols, int n, f32x4 v) {
+  if constexpr (BF16) {
+    uint16_t* p = static_cast<uint16_t*>(out) + row * n_cols + n;
+    const uint32_t lo = pack_bf16x2(v.x, v.y), hi = pack_bf16x2(v.z, v.w);
+    if (n + 4 <= n_cols && (n_cols & 3) == 0) {
+      *reinterpret_cast<u32x2*>(p) = u32x2{lo, hi};
+    } else {
+      if (n < n_cols) p[0] = (uint16_t)lo;
+      if (n + 1 < n_cols) p[1] = (uint16_t)(lo >> 16);
+      if (n + 2 < n_cols) p[2] = (uint16_t)hi;
+      if (n + 3 < n_cols) p[3] = (uint16_t)(hi >> 16);
+    }
+  } else {
+    float* p = static_cast<float*>(out) + row * n_cols + n;
+    if (n + 4 <= n_cols && (n_cols & 3) == 0) {
+      *reinterpret_cast<f32x4*>(p) = v;
+    } else {
+      if (n < n_cols) p[0] = v.x;
+      if (n + 1 < n_cols) p[1] = v.y;
+      if (n + 2 < n_cols) p[2] = v.z;
+      if (n + 3 < n_cols) p[3] = v.w;
+    }
+  }
+}
+
+}  // namespace fp4mi

@@ -1,5 +1,6 @@
 // MXFP4 products, dense and grouped by expert.
 #include <string.h>
+#include <utility>
 
 #include "fp4mi_ops.h"
 #include "host_common.hpp"
@@ -139,6 +140,16 @@ void launch_rows(ProductArgs p, int out_dtype, hipStream_t st) {
 // line-wide direct loads nor the 32-row fragment reads meet a bank twice.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+// f(integral_constant<int, 0>) .. f(integral_constant<int, N - 1>)
+template <typename F, int... I>
+__device__ __forceinline__ void unrolled_seq(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void unrolled(F f) {
+  unrolled_seq(f, std::make_integer_sequence<int, N>());
+}
+
 typedef __amdgpu_buffer_rsrc_t buffer_t;
 __device__ __forceinline__ buffer_t buffer_of(const void* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
@@ -155,34 +166,38 @@ __device__ __forceinline__ f32x16 mfma_scaled32(i32x4 a, i32x4 b, f32x16 c, int 
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, kE2M1, kE2M1, SA, sa, SB, sb);
 }
 
-// 16 scale bytes of a row of `bytes` >= 4 from byte `at`.  Past the row's end
+// 4 scale bytes of a row of `bytes` >= 4 from byte `at`.  Past the row's end
 // stand other bytes of the row: the codes there count as zero, and a NaN scale
 // among them makes the same outputs NaN by itself.  FULL: there are none.
 template <bool FULL>
-__device__ __forceinline__ i32x4 load_scales16(const uint8_t* row, int at, int bytes) {
-  i32x4 v;
-  if (FULL || at + 16 <= bytes) {
-    memcpy(&v, row + at, 16);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int want = at + 4 * i, have = min(want, bytes - 4);
-      uint32_t w;
-      memcpy(&w, row + have, 4);
-      v[i] = (int)(w >> (8 * min(want - have, 3)));
-    }
-  }
-  return v;
+__device__ __forceinline__ uint32_t load_scales4(const uint8_t* row, int at, int bytes) {
+  const int have = FULL ? at : min(at, bytes - 4);
+  uint32_t w;
+  memcpy(&w, row + have, 4);
+  return FULL ? w : w >> (8 * min(at - have, 3));
+}
+
+// Byte j of four words -> word j.
+__device__ __forceinline__ void transpose_bytes(const uint32_t (&w)[4], uint32_t (&t)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u);
+  const uint32_t b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+  const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
+  const uint32_t d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+  t[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+  t[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+  t[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+  t[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
 }
 
 template <int FN, int FM>
 struct TileShared {
   uint8_t w[2][64 * FN * 128];
   uint8_t x[2][64 * FM * 128];
-  // [k group][half of the rows][row % 32][row / 32 % F]: a lane's scale bytes
-  // of its wave's fragments are one word
-  uint8_t ws[2][8][2][32][FN];
-  uint8_t xs[2][8][2][32][FM];
+  // Scales of two pairs of stages: [pair][k group][half of the rows][row % 32],
+  // a word of the bytes of rows r, r + 32, r + 64, r + 96, the fragments of one
+  // wave (of both, where a wave has two).
+  uint32_t ws[2][16][2][32];
+  uint32_t xs[2][16][FM / 2][32];
 };
 
 template <int FN, int FM, bool BF16>
@@ -224,50 +239,52 @@ __global__ __launch_bounds__(256, 1) void product_tiles_kernel(ProductArgs p, in
   const buffer_t xb = buffer_of(xa, (int64_t)min(xrows, BM) * kb);
   // Stage s into buffer B.  In a last stage that reaches past K, the chunks
   // there are other bytes of the tile: mask() has them count as zero.
-  auto fetch = [&](auto b, auto full, int s) {
+  constexpr int kLoads = 2 * FN + 2 * FM;
+  auto fetch_one = [&](auto b, auto full, int s, int i) {
     constexpr int B = decltype(b)::value;
-    if (decltype(full)::value || s * 256 + 256 <= p.k) {
+    const bool isw = i < 2 * FN;
+    const int j = isw ? i : i - 2 * FN;
+    uint32_t v = isw ? wo[j] : xo[j], so = s * 128;
+    if (!decltype(full)::value && s * 256 + 256 > p.k) {
+      v += so - (uint32_t)max(s * 128 + ch * 16 + 16 - kb, 0);
+      so = 0;
+    }
+    if (isw) load_to_lds(wb, v, so, &sh.t.w[B][(wave * 2 * FN + j) * 1024]);
+    else load_to_lds(xb, v, so, &sh.t.x[B][(wave * 2 * FM + j) * 1024]);
+  };
+  auto fetch = [&](auto b, auto full, int s, int from, int to) {
 #pragma unroll
-      for (int i = 0; i < 2 * FN; ++i) load_to_lds(wb, wo[i], s * 128, &sh.t.w[B][(wave * 2 * FN + i) * 1024]);
+    for (int i = 0; i < kLoads; ++i)
+      if (i >= from && i < to) fetch_one(b, full, s, i);
+  };
+  // Scales: a thread loads 4 bytes (4 of a pair of stages' 16 k groups) of four
+  // rows and writes them as four words, one a k group.
+  const int seg = tid & 3, sr = (tid >> 2) & 31, sh2 = tid >> 7;
+  uint32_t wso[4], xso[4];
 #pragma unroll
-      for (int i = 0; i < 2 * FM; ++i) load_to_lds(xb, xo[i], s * 128, &sh.t.x[B][(wave * 2 * FM + i) * 1024]);
-    } else {
-      const uint32_t past = (uint32_t)max(s * 128 + ch * 16 + 16 - kb, 0);
+  for (int f = 0; f < 4; ++f) {
+    wso[f] = (uint32_t)min(sh2 * 128 + f * 32 + sr, wrows - 1) * (uint32_t)ksb;
+    xso[f] = (uint32_t)min((FM == 4 ? sh2 * 128 : 0) + f * 32 + sr, xrows - 1) * (uint32_t)ksb;
+  }
+  const uint8_t* xsc = static_cast<const uint8_t*>(p.a_scales) + (int64_t)row0 * ksb;
+  uint32_t wq[4], xq[4];
+  auto fetch_scales = [&](auto full, int s) {   // of stages s and s + 1
+    constexpr bool FULL = decltype(full)::value;
 #pragma unroll
-      for (int i = 0; i < 2 * FN; ++i) load_to_lds(wb, wo[i] + s * 128 - past, 0, &sh.t.w[B][(wave * 2 * FN + i) * 1024]);
-#pragma unroll
-      for (int i = 0; i < 2 * FM; ++i) load_to_lds(xb, xo[i] + s * 128 - past, 0, &sh.t.x[B][(wave * 2 * FM + i) * 1024]);
+    for (int f = 0; f < 4; ++f) {
+      wq[f] = load_scales4<FULL>(ws + wso[f], s * 8 + seg * 4, ksb);
+      xq[f] = load_scales4<FULL>(xsc + xso[f], s * 8 + seg * 4, ksb);
     }
   };
-  // Scales: thread t owns row t of W's tile and row t % BM of X's; 16 bytes
-  // serve two stages.
-  const uint8_t* wsp = ws + (int64_t)min(tid, wrows - 1) * ksb;
-  const uint8_t* xsp = static_cast<const uint8_t*>(p.a_scales) +
-                       (int64_t)(row0 + min(tid % BM, xrows - 1)) * ksb;
-  i32x4 wsc, xsc;
-  auto fetch_scales = [&](auto full, int s) {
-    wsc = load_scales16<decltype(full)::value>(wsp, s * 8, ksb);
-    xsc = load_scales16<decltype(full)::value>(xsp, s * 8, ksb);
-  };
-  // of the pair's first or second stage; with half as many X rows, thread t
-  // and t + BM write half of row t's bytes each
-  uint8_t* wput = &sh.t.ws[0][0][tid / (32 * FN)][tid & 31][(tid >> 5) % FN];
-  const int xr = tid % BM, xj = tid / BM * (8 * BM / 256);
-  uint8_t* xput = &sh.t.xs[0][xj][xr / (32 * FM)][xr & 31][(xr >> 5) % FM];
-  auto put_scales = [&](auto b) {
-    constexpr int B = decltype(b)::value;
+  auto put_scales = [&](int s) {
+    uint32_t t[4];
+    const int pair = (s >> 1) & 1;
+    transpose_bytes(wq, t);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      wput[(B * 8 + j) * 64 * FN] = (uint8_t)((uint32_t)wsc[2 * B + (j >> 2)] >> (8 * (j & 3)));
-    if constexpr (FM == 4) {
+    for (int j = 0; j < 4; ++j) sh.t.ws[pair][seg * 4 + j][sh2][sr] = t[j];
+    transpose_bytes(xq, t);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        xput[(B * 8 + j) * 64 * FM] = (uint8_t)((uint32_t)xsc[2 * B + (j >> 2)] >> (8 * (j & 3)));
-    } else {
-        const uint32_t v = (uint32_t)(tid < BM ? xsc[2 * B] : xsc[2 * B + 1]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) xput[(B * 8 + j) * 64 * FM] = (uint8_t)(v >> (8 * j));
-    }
+    for (int j = 0; j < 4; ++j) sh.t.xs[pair][seg * 4 + j][FM == 4 ? sh2 : 0][sr] = t[j];
   };
 
   const int r = lane & 31, g = lane >> 5;
@@ -282,32 +299,30 @@ __global__ __launch_bounds__(256, 1) void product_tiles_kernel(ProductArgs p, in
     wl[ks] = &sh.t.w[0][(wn * FN * 32 + r) * 128 + c];
     xl[ks] = &sh.t.x[0][(wm * FM * 32 + r) * 128 + c];
   }
-  const uint8_t *wsl = &sh.t.ws[0][g][wn][r][0], *xsl = &sh.t.xs[0][g][wm][r][0];
-  auto read = [&](auto b, int ks, Step& o) {   // 64 k of a stage
+  // Of 64 k of stage s, the scales (i = 0) or fragment i - 1 of both operands.
+  auto read_part = [&](auto b, int s, int ks, int i, Step& o) {
     constexpr int B = decltype(b)::value;
-#pragma unroll
-    for (int f = 0; f < FN; ++f)
-      o.w[f] = *reinterpret_cast<const i32x4*>(wl[ks] + (B * BN + f * 32) * 128);
-#pragma unroll
-    for (int f = 0; f < FM; ++f)
-      o.x[f] = *reinterpret_cast<const i32x4*>(xl[ks] + (B * BM + f * 32) * 128);
-    o.ws = *reinterpret_cast<const int*>(wsl + (B * 8 + 2 * ks) * 64 * FN);
-    if constexpr (FM == 4)
-      o.xs = *reinterpret_cast<const int*>(xsl + (B * 8 + 2 * ks) * 64 * FM);
-    else
-      o.xs = *reinterpret_cast<const uint16_t*>(xsl + (B * 8 + 2 * ks) * 64 * FM);
+    if (i == 0) {
+      const int pair = (s >> 1) & 1;
+      o.ws = (int)sh.t.ws[pair][B * 8 + 2 * ks + g][wn][r];
+      o.xs = FM == 4 ? (int)sh.t.xs[pair][B * 8 + 2 * ks + g][wm][r]
+                     : (int)(sh.t.xs[pair][B * 8 + 2 * ks + g][0][r] >> (16 * wm));
+      return;
+    }
+    const int f = i - 1;
+    o.w[f] = *reinterpret_cast<const i32x4*>(wl[ks] + (B * BN + f * 32) * 128);
+    if (f < FM) o.x[f] = *reinterpret_cast<const i32x4*>(xl[ks] + (B * BM + f * 32) * 128);
   };
   f32x16 acc[FN][FM] = {};
-  auto multiply = [&](const Step& o) {
-#define FP4MI_ROW(I)                                                                   \
-  acc[I][0] = mfma_scaled32<I, 0>(o.w[I], o.x[0], acc[I][0], o.ws, o.xs);              \
-  acc[I][1] = mfma_scaled32<I, 1>(o.w[I], o.x[1], acc[I][1], o.ws, o.xs);              \
-  if constexpr (FM == 4) {                                                             \
-    acc[I][FM - 2] = mfma_scaled32<I, 2>(o.w[I], o.x[FM - 2], acc[I][FM - 2], o.ws, o.xs); \
-    acc[I][FM - 1] = mfma_scaled32<I, 3>(o.w[I], o.x[FM - 1], acc[I][FM - 1], o.ws, o.xs); \
-  }
-    FP4MI_ROW(0) FP4MI_ROW(1) FP4MI_ROW(2) FP4MI_ROW(3)
-#undef FP4MI_ROW
+  // The FN FM products of a step, between(i) after product i; both stay where
+  // they are written.
+  auto multiply = [&](const Step& o, auto between) {
+    unrolled<FN * FM>([&](auto idx) {
+      constexpr int I = decltype(idx)::value / FM, J = decltype(idx)::value % FM;
+      acc[I][J] = mfma_scaled32<I, J>(o.w[I], o.x[J], acc[I][J], o.ws, o.xs);
+      between(idx);
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
   // Past K in the last stage W's codes count as zero.
   auto mask = [&](int s, int ks, Step& o) {
@@ -326,41 +341,54 @@ __global__ __launch_bounds__(256, 1) void product_tiles_kernel(ProductArgs p, in
   constexpr std::true_type yes{};
   constexpr std::false_type no{};
   fetch_scales(no, 0);
-  fetch(first, no, 0);
-  put_scales(first);
+  fetch(first, no, 0, 0, kLoads);
+  put_scales(0);
+  if (stages > 2) fetch_scales(no, 2);
   landed();
   Step even, odd;
-  read(first, 0, even);
-  if (stages > 1) fetch(second, no, 1);
-  // Stage s in buffer b, the next in nb.  MID: stages s + 1, s + 2 and, where b
-  // is the first, s + 3 follow and end inside K; then nothing here branches, and
-  // the loads, reads and products stay in the order written.
+#pragma unroll
+  for (int i = 0; i <= FN; ++i) read_part(first, 0, 0, i, even);
+  if (stages > 1) fetch(second, no, 1, 0, kLoads / 2);
+  // Stage s in buffer b, the next in nb.  MID: stages s + 1 and s + 2 follow and
+  // end inside K; where b is the first, so do the scales of s + 4 and s + 5;
+  // then nothing here branches.
+  // The direct loads of a stage are spread over the 16 products that follow the
+  // barrier and the 16 after those: issued together they would hold the wave up.
+  constexpr int kAll = FN * FM;
   auto stage = [&](auto b, auto nb, auto mid, int s) {
     constexpr bool MID = decltype(mid)::value;
-    const bool more = MID || s + 1 < stages;
-    read(b, 1, odd);
+    const bool more = MID || s + 1 < stages, more2 = MID || s + 2 < stages;
+    auto reads = [&](auto bb, int st, int ks, Step& o, int i) {
+      if (i <= FN) read_part(bb, st, ks, i, o);
+    };
+    auto loads = [&](auto bb, int st, int half, int i) {   // one of half the loads every other product
+      constexpr int every = 2 * kAll / kLoads > 1 ? 2 * kAll / kLoads : 1;
+      if (i % every == every - 1 && i / every < kLoads / 2) fetch_one(bb, mid, st, half * (kLoads / 2) + i / every);
+    };
     if (!MID) mask(s, 0, even);
-    multiply(even);
-    __builtin_amdgcn_sched_barrier(0);
-    read(b, 2, even);
-    if (more) put_scales(nb);
-    if (decltype(b)::value == 0 && (MID || s + 2 < stages)) fetch_scales(mid, s + 2);
+    multiply(even, [&](auto i) {
+      reads(b, s, 1, odd, i);
+      if (more) loads(nb, s + 1, 1, i);
+    });
     if (!MID) mask(s, 1, odd);
-    multiply(odd);
-    __builtin_amdgcn_sched_barrier(0);
-    read(b, 3, odd);
+    multiply(odd, [&](auto i) {
+      reads(b, s, 2, even, i);
+      if (decltype(b)::value == 0 && i == kAll - 2 && more2) put_scales(s + 2);
+    });
     if (!MID) mask(s, 2, even);
-    multiply(even);
-    __builtin_amdgcn_sched_barrier(0);
+    multiply(even, [&](auto i) {
+      reads(b, s, 3, odd, i);
+      if (decltype(b)::value == 0 && i == FN + 1 && (MID || s + 4 < stages)) fetch_scales(mid, s + 4);
+    });
     landed();   // stage s + 1; and everyone has read stage s
-    if (more) read(nb, 0, even);
-    if (MID || s + 2 < stages) fetch(b, mid, s + 2);
     if (!MID) mask(s, 3, odd);
-    multiply(odd);
-    __builtin_amdgcn_sched_barrier(0);
+    multiply(odd, [&](auto i) {
+      if (more) reads(nb, s + 1, 0, even, i);
+      if (more2) loads(b, s + 2, 0, i);
+    });
   };
   int s = 0;
-  for (; s + 4 <= (p.k >> 8); s += 2) {
+  for (; s + 6 <= (p.k >> 8); s += 2) {
     stage(first, second, yes, s);
     stage(second, first, yes, s + 1);
   }

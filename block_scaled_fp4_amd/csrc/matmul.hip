@@ -138,18 +138,6 @@ void launch_rows(ProductArgs p, int out_dtype, hipStream_t st) {
 // to LDS with direct loads, two stages in turn, one barrier each.  A row's
 // eight 16-byte chunks lie at position chunk ^ (row % 8), so that neither the
 // line-wide direct loads nor the 32-row fragment reads meet a bank twice.
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-// f(integral_constant<int, 0>) .. f(integral_constant<int, N - 1>)
-template <typename F, int... I>
-__device__ __forceinline__ void unrolled_seq(F f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>()), ...);
-}
-template <int N, typename F>
-__device__ __forceinline__ void unrolled(F f) {
-  unrolled_seq(f, std::make_integer_sequence<int, N>());
-}
-
 typedef __amdgpu_buffer_rsrc_t buffer_t;
 __device__ __forceinline__ buffer_t buffer_of(const void* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
@@ -206,7 +194,7 @@ __global__ __launch_bounds__(256, 1) void product_tiles_kernel(ProductArgs p, in
   constexpr int BN = 64 * FN, BM = 64 * FM;
   __shared__ __align__(16) union {
     TileShared<FN, FM> t;
-    uint8_t out[4][32 * (32 * FN * 4 + 16)];
+    uint8_t out[4][quarter_bytes<FN, BF16>()];
   } sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t blk = (int64_t)blockIdx.x + blk0;
@@ -397,40 +385,9 @@ __global__ __launch_bounds__(256, 1) void product_tiles_kernel(ProductArgs p, in
     if (s + 1 < stages) stage(second, first, no, s + 1);
   }
 
-  // Each wave turns its quarter through LDS, 32 tokens at a time, so that a
-  // token's columns leave as whole lines.
-  constexpr int kRow = 32 * FN * (BF16 ? 2 : 4) + 16;
-  uint8_t* buf = sh.out[wave];
-  const int nw = n0 + wn * 32 * FN;
   __syncthreads();
-#pragma unroll
-  for (int fm = 0; fm < FM; ++fm) {
-    const int mbase = row0 + (wm * FM + fm) * 32;
-    const float rs = p.a_row_scale ? p.a_row_scale[min(mbase + r, row_end - 1)] : 1.0f;
-#pragma unroll
-    for (int fn = 0; fn < FN; ++fn)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = fn * 32 + 8 * q + 4 * g;
-        const f32x16& c = acc[fn][fm];
-        const f32x4 v = {c[4 * q] * rs, c[4 * q + 1] * rs, c[4 * q + 2] * rs, c[4 * q + 3] * rs};
-        if constexpr (BF16)
-          *reinterpret_cast<u32x2*>(buf + r * kRow + n * 2) =
-              u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
-        else
-          *reinterpret_cast<f32x4*>(buf + r * kRow + n * 4) = v;
-      }
-    __builtin_amdgcn_wave_barrier();
-    constexpr int kLanes = 32 * FN * (BF16 ? 2 : 4) / 16;   // lanes a row takes
-    constexpr int kEl = BF16 ? 8 : 4;
-#pragma unroll
-    for (int it = 0; it < 32 * kLanes / 64; ++it) {
-      const int m = it * (64 / kLanes) + lane / kLanes, n = (lane % kLanes) * kEl;
-      if (mbase + m < row_end)
-        store_chunk<BF16>(p.out, mbase + m, p.n, nw + n, buf + m * kRow + (lane % kLanes) * 16);
-    }
-    __builtin_amdgcn_wave_barrier();
-  }
+  store_quarter<FN, FM, BF16>(acc, sh.out[wave], p.out, row0 + wm * FM * 32, row_end, p.n,
+                              n0 + wn * FN * 32, p.a_row_scale);
 }
 
 template <int FN, int FM>
@@ -444,10 +401,90 @@ void launch_tiles(ProductArgs p, int out_dtype, hipStream_t st) {
     launch_1d(product_tiles_kernel<FN, FM, false>, blocks, 256, st, p);
 }
 
+// FP8 rows by MXFP4, see bf16_tile.
+template <bool BF16>
+__global__ __launch_bounds__(256, 2) void product_fp8_tiles_kernel(ProductArgs p, int64_t blk0) {
+  __shared__ __align__(16) union {
+    Bf16Shared<false> t;
+    uint8_t out[4][quarter_bytes<4, BF16>()];
+  } sh;
+  const int64_t blk = (int64_t)blockIdx.x + blk0;
+  const int nt = (int)(blk % p.n_tiles), mt = (int)(blk / p.n_tiles);
+  int e = 0, row0 = mt * kBM, row_end = (int)p.tokens;
+  if (p.offsets) {
+    if (!locate_tile<kBM>(p.offsets, p.experts, (int)p.tokens, mt, e, row0, row_end)) return;
+  }
+  const int n0 = nt * kBN, kb = p.k >> 1, ksb = p.k >> 5, kx = p.k >> 7;
+  const int wrows = p.n - n0, xrows = row_end - row0;
+  const uint8_t* w = p.w + ((int64_t)e * p.n + n0) * kb;
+  const uint8_t* ws = p.w_scales + ((int64_t)e * p.n + n0) * ksb;
+  const uint8_t* x = p.a + (int64_t)row0 * p.k;
+  const float* xs = static_cast<const float*>(p.a_scales) + (int64_t)row0 * kx;
+  f32x16 acc[4][2] = {};
+  const bool odd = bf16_tile<false>(
+      sh.t, kx, kx,
+      [&](auto, int s, int row, int c) {
+        return *reinterpret_cast<const i32x4*>(w + (int64_t)min(row, wrows - 1) * kb + s * 64 + c * 16);
+      },
+      [&](auto, int s, int row, int c) {
+        return *reinterpret_cast<const i32x4*>(x + (int64_t)min(row, xrows - 1) * p.k + s * 128 + c * 16);
+      },
+      [&](auto, int s, int row) {
+        return *reinterpret_cast<const uint32_t*>(ws + (int64_t)min(row, wrows - 1) * ksb + s * 4);
+      },
+      [&](int s, int row) { return e8m0_of(xs[(int64_t)min(row, xrows - 1) * kx + s]); }, acc);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m0 = row0 + (wave >> 1) * 64, nw = n0 + (wave & 1) * 128;
+  const auto slow = [&]() {   // whether a scale outside the window has codes to scale
+    bool bad = false;
+    const int wr = min((int)threadIdx.x, wrows - 1), xr = min((int)threadIdx.x % kBM, xrows - 1);
+    for (int i = 0; i < 4 * kx; ++i) {
+      LaneStep<false> lw;
+      LaneStep<true> lx;
+      load_lane<false, false>(w, ws, wr, p.k, i >> 2, i & 3, lw);
+      load_lane<true, false>(x, xs, xr, p.k, i >> 2, i & 3, lx);
+      bad |= !scale_fits(lw) || !scale_fits(lx);
+    }
+    return bad;
+  };
+  if (__syncthreads_or(odd) && __syncthreads_or(slow())) {
+    // rare: 16 x 16 at a time, straight from memory, with every scale's range
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    for (int i = 0; i < 32; ++i) {
+      const int m = m0 + (i >> 3) * 16, n = nw + (i & 7) * 16;
+      LaneStep<false> lw[1];
+      LaneStep<true> lx[1];
+      f32x4 c[1][1] = {};
+      for (int s = 0; s < kx; ++s) {
+        load_lane<false, false>(w, ws, min(n + r, p.n - 1) - n0, p.k, s, g, lw[0]);
+        load_lane<true, false>(x, xs, min(m + r, row_end - 1) - row0, p.k, s, g, lx[0]);
+        mfma_bf16_step(lw, lx, c);
+      }
+      if (m + r < row_end) {
+        if (p.a_row_scale) c[0][0] *= p.a_row_scale[m + r];
+        store_out4<BF16>(p.out, m + r, p.n, n + 4 * g, c[0][0]);
+      }
+    }
+    return;
+  }
+  store_quarter<4, 2, BF16>(acc, sh.out[wave], p.out, m0, row_end, p.n, nw, p.a_row_scale);
+}
+
+void launch_fp8_tiles(ProductArgs p, int out_dtype, hipStream_t st) {
+  p.n_tiles = (p.n + kBN - 1) / kBN;
+  const int64_t blocks = p.n_tiles * max_row_tiles(p.tokens, p.experts, kBM, p.offsets != nullptr);
+  if (out_dtype == FP4_DTYPE_BF16)
+    launch_1d(product_fp8_tiles_kernel<true>, blocks, 256, st, p);
+  else
+    launch_1d(product_fp8_tiles_kernel<false>, blocks, 256, st, p);
+}
+
 template <bool A8, bool KT>
 void launch_product(const ProductArgs& p, int out_dtype, hipStream_t st) {
-  if constexpr (!A8) {
-    const int64_t per = p.tokens / p.experts;
+  const int64_t per = p.tokens / p.experts;
+  if constexpr (A8) {
+    if (per >= 128) return launch_fp8_tiles(p, out_dtype, st);
+  } else {
     if (per >= 512) return launch_tiles<4, 4>(p, out_dtype, st);
     if (per >= 128) return launch_tiles<4, 2>(p, out_dtype, st);
   }

@@ -11,6 +11,7 @@
 #pragma once
 
 #include <type_traits>
+#include <utility>
 
 #include "device_common.hpp"
 
@@ -19,6 +20,7 @@ namespace fp4mi {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kE2M1 = 4;   // the instruction's operand format field
 
@@ -275,6 +277,182 @@ __device__ __forceinline__ void store_chunk(void* out, int64_t row, int n_cols, 
         reinterpret_cast<uint32_t*>(dst)[j] = reinterpret_cast<const uint32_t*>(src)[j];
     }
   }
+}
+
+// f(integral_constant<int, 0>) .. f(integral_constant<int, N - 1>)
+template <typename F, int... I>
+__device__ __forceinline__ void unrolled_seq(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void unrolled(F f) {
+  unrolled_seq(f, std::make_integer_sequence<int, N>());
+}
+
+// A wave's quarter of a tile, 32 FN columns from `n0` by 32 FM tokens from
+// `m0`, in 32 x 32 fragments (D's lane l: column l % 32 = the token, rows
+// 8 (i / 4) + 4 (l / 32) + i % 4 = the columns of the output).  32 tokens at a
+// time are turned through `buf`, so that a token's columns leave as whole lines
+// and not as 16 bytes each; the padding keeps the rows on different banks.
+template <int FN, bool BF16>
+constexpr int quarter_bytes() {
+  return 32 * (32 * FN * (BF16 ? 2 : 4) + 16);
+}
+template <int FN, int FM, bool BF16>
+__device__ __forceinline__ void store_quarter(const f32x16 (&acc)[FN][FM], uint8_t* buf, void* out,
+                                              int64_t m0, int64_t row_end, int n_cols, int n0,
+                                              const float* row_scale) {
+  constexpr int kRow = quarter_bytes<FN, BF16>() / 32;
+  constexpr int kLanes = 32 * FN * (BF16 ? 2 : 4) / 16, kEl = BF16 ? 8 : 4;   // lanes a row takes
+  const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
+#pragma unroll
+  for (int fm = 0; fm < FM; ++fm) {
+    const int64_t mbase = m0 + fm * 32;
+    const int64_t m = mbase + r < row_end ? mbase + r : row_end - 1;
+    const float rs = row_scale ? row_scale[m] : 1.0f;
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = fn * 32 + 8 * q + 4 * g;
+        const f32x16& c = acc[fn][fm];
+        const f32x4 v = {c[4 * q] * rs, c[4 * q + 1] * rs, c[4 * q + 2] * rs, c[4 * q + 3] * rs};
+        if constexpr (BF16)
+          *reinterpret_cast<u32x2*>(buf + r * kRow + n * 2) =
+              u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+        else
+          *reinterpret_cast<f32x4*>(buf + r * kRow + n * 4) = v;
+      }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int it = 0; it < 32 * kLanes / 64; ++it) {
+      const int t = it * (64 / kLanes) + lane / kLanes, n = (lane % kLanes) * kEl;
+      if (mbase + t < row_end)
+        store_chunk<BF16>(out, mbase + t, n_cols, n0 + n, buf + t * kRow + (lane % kLanes) * 16);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// ------------------------------------------------ tiles of bf16 products
+// The E4M3 products at size: one workgroup of four waves owns 256 rows of
+// operand A (the output's columns) by 128 of operand B, each wave 128 x 64 of
+// them in 32 x 32 x 16 instructions.  A stage is 128 k.  Codes are staged
+// through registers into LDS as they are, two stages in turn with one barrier
+// each, and become bf16 values on their way to the instructions.
+//
+// E4M3 rows are 8 chunks of 16 bytes, chunk c at position c ^ (row % 8); E2M1
+// rows are 4 chunks, c at c ^ (row / 2 % 4): eight consecutive rows then touch
+// every bank once.  Scales lie beside as bytes, one a row (E4M3, one block of
+// 128) or four (E2M1).
+constexpr int kBN = 256, kBM = 128;
+
+template <bool A8>
+struct Bf16Shared {
+  static constexpr int kA = A8 ? 128 : 64;   // bytes of a row of A
+  uint8_t a[2][kBN * kA];
+  uint8_t b[2][kBM * 128];
+  uint8_t as[2][kBN * (A8 ? 1 : 4)];
+  uint8_t bs[2][kBM];
+};
+
+template <bool F8>
+__device__ __forceinline__ int chunk_at(int row, int c) {
+  return F8 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+}
+
+// load_a(s, row, chunk), load_b: 16 bytes of stage s; scale_a(s, row): its four
+// bytes (E2M1) or one (E4M3), scale_b: one.  mid: the stages whose loads need
+// no care at the end of K.  Returns whether some scale this thread loaded was
+// outside the bf16 window.
+template <bool A8, typename LA, typename LB, typename SA, typename SB>
+__device__ __forceinline__ bool bf16_tile(Bf16Shared<A8>& sh, int stages, int full_stages, LA load_a,
+                                          LB load_b, SA scale_a, SB scale_b, f32x16 (&acc)[4][2]) {
+  constexpr int kPerA = Bf16Shared<A8>::kA / 16, kLA = kBN * kPerA / 256, kLB = kBM * 8 / 256;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave & 1, wm = wave >> 1, r = lane & 31, g = lane >> 5;
+  i32x4 ra[kLA], rb[kLB];
+  uint32_t sa = 0, sb = 0;
+  bool odd_scale = false;
+  auto fetch = [&](auto full, int s) {
+#pragma unroll
+    for (int i = 0; i < kLA; ++i) ra[i] = load_a(full, s, (i * 256 + tid) / kPerA, tid % kPerA);
+#pragma unroll
+    for (int i = 0; i < kLB; ++i) rb[i] = load_b(full, s, (i * 256 + tid) / 8, tid % 8);
+    sa = scale_a(full, s, tid);
+    sb = scale_b(s, tid % kBM);
+  };
+  auto put = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < kLA; ++i)
+      *reinterpret_cast<i32x4*>(&sh.a[b][chunk_at<A8>((i * 256 + tid) / kPerA, tid % kPerA)]) = ra[i];
+#pragma unroll
+    for (int i = 0; i < kLB; ++i)
+      *reinterpret_cast<i32x4*>(&sh.b[b][chunk_at<true>((i * 256 + tid) / 8, tid % 8)]) = rb[i];
+    if constexpr (A8) {
+      sh.as[b][tid] = (uint8_t)sa;
+      odd_scale |= !scale_in_window((int)sa);
+    } else {
+      reinterpret_cast<uint32_t*>(sh.as[b])[tid] = sa;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) odd_scale |= !scale_in_window((int)((sa >> (8 * j)) & 0xFFu));
+    }
+    sh.bs[b][tid % kBM] = (uint8_t)sb;
+    odd_scale |= !scale_in_window((int)sb);
+  };
+  auto compute = [&](int b) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      bf16x8_t y[2][4];
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int row = (wm * 2 + f) * 32 + r;
+        Frag<true> v;
+        v.lo = *reinterpret_cast<const i32x4*>(&sh.b[b][chunk_at<true>(row, 4 * ks + 2 * g)]);
+        v.hi = *reinterpret_cast<const i32x4*>(&sh.b[b][chunk_at<true>(row, 4 * ks + 2 * g + 1)]);
+        const float sc = scale_of(sh.bs[b][row]);
+        unrolled<4>([&](auto q) { y[f][q] = bf16_of<decltype(q)::value>(v, sc); });
+      }
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int row = (wn * 4 + f) * 32 + r;
+        Frag<A8> v;
+        float sc;
+        if constexpr (A8) {
+          v.lo = *reinterpret_cast<const i32x4*>(&sh.a[b][chunk_at<true>(row, 4 * ks + 2 * g)]);
+          v.hi = *reinterpret_cast<const i32x4*>(&sh.a[b][chunk_at<true>(row, 4 * ks + 2 * g + 1)]);
+          sc = scale_of(sh.as[b][row]);
+        } else {
+          v.lo = *reinterpret_cast<const i32x4*>(&sh.a[b][chunk_at<false>(row, 2 * ks + g)]);
+          sc = scale_of(sh.as[b][row * 4 + 2 * ks + g]);
+        }
+        unrolled<4>([&](auto q) {
+          const bf16x8_t x = bf16_of<decltype(q)::value>(v, sc);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[f][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y[j][q], acc[f][j], 0, 0, 0);
+        });
+      }
+    }
+  };
+  if (stages == 0) return false;
+  fetch(std::false_type(), 0);
+  put(0);
+  __syncthreads();
+  int s = 0;
+  for (; s + 1 < full_stages; ++s) {
+    fetch(std::true_type(), s + 1);
+    compute(s & 1);
+    put((s + 1) & 1);
+    __syncthreads();
+  }
+  for (; s < stages; ++s) {
+    if (s + 1 < stages) fetch(std::false_type(), s + 1);
+    compute(s & 1);
+    if (s + 1 < stages) put((s + 1) & 1);
+    __syncthreads();
+  }
+  return odd_scale;
 }
 
 }  // namespace fp4mi

@@ -42,43 +42,96 @@ __device__ __forceinline__ Frag<true> load_tokens(const uint8_t* ch, int t, int 
   return f;
 }
 
-// One wave per 64 x 64 tile of one expert's gradient, operands straight from
-// memory.  N is operand A of the instruction, so a lane ends with four
-// consecutive columns of one row of out.
 struct LaneTokens {
   Frag<true> v;
   int s;
 };
-constexpr int kWF = 4;
+
+// 16 tokens from t; FULL: all inside the shard.
+template <bool FULL>
+__device__ __forceinline__ i32x4 load_tokens16(const uint8_t* ch, int t, int count) {
+  i32x4 v;
+  if (FULL || t + 16 <= count) {
+    memcpy(&v, ch + t, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (t + 4 * i + b < count) w |= (uint32_t)ch[t + 4 * i + b] << (8 * b);
+      v[i] = (int)w;
+    }
+  }
+  return v;
+}
+
+// See bf16_tile: channels of b are its operand A (consecutive columns of the
+// output), channels of a its operand B, tokens its k.
 template <bool BF16>
-__global__ __launch_bounds__(64) void wgrad_kernel(WgradArgs p, int64_t blk0) {
+__global__ __launch_bounds__(256, 1) void wgrad_tiles_kernel(WgradArgs p, int64_t blk0) {
+  __shared__ __align__(16) union {
+    Bf16Shared<true> t;
+    uint8_t out[4][quarter_bytes<4, BF16>()];
+  } sh;
   const int64_t blk = (int64_t)blockIdx.x + blk0;
   const int nt = (int)(blk % p.n_tiles), mt = (int)((blk / p.n_tiles) % p.m_tiles);
   const int e = (int)(blk / ((int64_t)p.n_tiles * p.m_tiles));
-  const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
   int lo, hi;
   shard_bounds(p.offsets, e, p.tokens, lo, hi);
   const int cnt = hi - lo, blocks = (cnt + 127) >> 7;
   const int64_t sblk = ((int64_t)lo + 127) / 128 + e;
-  const int m0 = mt * 16 * kWF, n0 = nt * 16 * kWF;
-  f32x4 acc[kWF][kWF] = {};
-  for (int j = 0; j < blocks; ++j) {
-    LaneTokens a[kWF], b[kWF];
-#pragma unroll
-    for (int f = 0; f < kWF; ++f) {
-      const int n = n0 + 16 * f + r, m = m0 + 16 * f + r;
-      b[f].v = load_tokens(p.b + (int64_t)p.n * lo + (int64_t)n * cnt, 128 * j + 32 * g, cnt);
-      b[f].s = (int)e8m0_of(p.b_scales[sblk * p.n + (int64_t)n * blocks + j]);
-      a[f].v = load_tokens(p.a + (int64_t)p.m * lo + (int64_t)m * cnt, 128 * j + 32 * g, cnt);
-      a[f].s = (int)e8m0_of(p.a_scales[sblk * p.m + (int64_t)m * blocks + j]);
+  const int m0 = mt * kBM, n0 = nt * kBN, nrows = p.n - n0;
+  const uint8_t* a = p.a + (int64_t)p.m * lo + (int64_t)m0 * cnt;
+  const uint8_t* b = p.b + (int64_t)p.n * lo + (int64_t)n0 * cnt;
+  const float* as = p.a_scales + sblk * p.m + (int64_t)m0 * blocks;
+  const float* bs = p.b_scales + sblk * p.n + (int64_t)n0 * blocks;
+  f32x16 acc[4][2] = {};
+  const bool odd = bf16_tile<true>(
+      sh.t, blocks, cnt >> 7,
+      [&](auto full, int s, int row, int c) {
+        return load_tokens16<decltype(full)::value>(b + (int64_t)min(row, nrows - 1) * cnt, s * 128 + c * 16, cnt);
+      },
+      [&](auto full, int s, int row, int c) {
+        return load_tokens16<decltype(full)::value>(a + (int64_t)row * cnt, s * 128 + c * 16, cnt);
+      },
+      [&](auto, int s, int row) { return e8m0_of(bs[(int64_t)min(row, nrows - 1) * blocks + s]); },
+      [&](int s, int row) { return e8m0_of(as[(int64_t)row * blocks + s]); }, acc);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int mw = m0 + (wave >> 1) * 64, nw = n0 + (wave & 1) * 128;
+  const int64_t orow = (int64_t)e * p.m;
+  auto lane_tokens = [&](const uint8_t* ch, const float* sc, int row, int s, int g, LaneTokens& l) {
+    l.v = load_tokens(ch + (int64_t)row * cnt, 128 * s + 32 * g, cnt);
+    l.s = (int)e8m0_of(sc[(int64_t)row * blocks + s]);
+  };
+  const auto slow = [&]() {   // whether a scale outside the window has codes to scale
+    bool bad = false;
+    for (int i = 0; i < 4 * blocks; ++i) {
+      LaneTokens lb, la;
+      lane_tokens(b, bs, min((int)threadIdx.x, nrows - 1), i >> 2, i & 3, lb);
+      lane_tokens(a, as, threadIdx.x % kBM, i >> 2, i & 3, la);
+      bad |= !scale_fits(lb) || !scale_fits(la);
     }
-    mfma_bf16_step(b, a, acc);
+    return bad;
+  };
+  if (__syncthreads_or(odd) && __syncthreads_or(slow())) {
+    // rare: 16 x 16 at a time, straight from memory, with every scale's range
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    if (nw >= p.n) return;
+    for (int i = 0; i < 32; ++i) {
+      const int m = mw + (i >> 3) * 16, n = nw + (i & 7) * 16;
+      LaneTokens lb[1], la[1];
+      f32x4 c[1][1] = {};
+      for (int s = 0; s < blocks; ++s) {
+        lane_tokens(b, bs, n - n0 + r, s, g, lb[0]);
+        lane_tokens(a, as, m - m0 + r, s, g, la[0]);
+        mfma_bf16_step(lb, la, c);
+      }
+      store_out4<BF16>(p.out, orow + m + r, p.n, n + 4 * g, c[0][0]);
+    }
+    return;
   }
-#pragma unroll
-  for (int x = 0; x < kWF; ++x)
-#pragma unroll
-    for (int y = 0; y < kWF; ++y)
-      store_out4<BF16>(p.out, (int64_t)e * p.m + m0 + 16 * y + r, p.n, n0 + 16 * x + 4 * g, acc[x][y]);
+  store_quarter<4, 2, BF16>(acc, sh.out[wave], p.out, orow + mw, orow + p.m, p.n, nw, nullptr);
 }
 
 }  // namespace
@@ -114,13 +167,13 @@ extern "C" int fp8_matmul_tokblk(const uint8_t* a, const float* a_scales, const 
   for (int i = 0; i < 5; ++i)
     if (overlaps(out, n_out * osz, ins[i], inn[i])) return FP4_EOVERLAP;
   WgradArgs p = {a, a_scales, b, b_scales, token_offsets, out, (int)T, (int)M, (int)N,
-                 (int)(M / (16 * kWF)), (int)(N / (16 * kWF))};
+                 (int)(M / kBM), (int)((N + kBN - 1) / kBN)};
   clear_stale_error();
   hipStream_t st = as_stream(stream);
   const int64_t grid = E * p.m_tiles * p.n_tiles;
   if (out_dtype == FP4_DTYPE_BF16)
-    launch_1d(wgrad_kernel<true>, grid, 64, st, p);
+    launch_1d(wgrad_tiles_kernel<true>, grid, 256, st, p);
   else
-    launch_1d(wgrad_kernel<false>, grid, 64, st, p);
+    launch_1d(wgrad_tiles_kernel<false>, grid, 256, st, p);
   return launch_status();
 }

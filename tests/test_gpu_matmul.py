@@ -274,3 +274,34 @@ def test_binding_refuses():
         m.mxfp4_matmul(a, sa, a, sa, out_dtype=torch.float16)
     with pytest.raises(m.Fp4Error):                                 # out over an input
         m.mxfp4_matmul(a, sa, a, sa, out=a.view(-1)[:64].view(torch.float32).view(4, 4))
+
+
+def test_large_fp8_tiles_with_scales_out_of_window():
+    """Shapes that take the tiles: blocks of zeros with the smallest scale,
+    a far smaller and a far larger scale over codes, and NaN scales."""
+    m = need_gpu()
+    rng = np.random.default_rng(31)
+    M, N, K = 300, 330, 512
+    q, s = R.random_fp8(rng, M, K)
+    qb, sb = R.random_mx(rng, N, K)
+    q[5] = 0
+    s[5] = 2.0 ** -127
+    codes = F.unpack_codes(qb)
+    codes[7, 64:96] = 8                                  # negative zeros
+    qb = F.pack_codes(codes)
+    sb[7, 2] = 0
+    for step in range(3):
+        if step == 1:
+            s[140, 1] = 2.0 ** -120
+            sb[9, 3] = 240
+        if step == 2:
+            sb[200, 4] = 255
+        c = m.mxfp4_matmul(dev_u8(q), dev_f32(s), dev_u8(qb), dev_u8(sb), out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        got = host(c)
+        if step == 2:
+            assert np.isnan(got[:, 200]).all() and not np.isnan(np.delete(got, 200, 1)).any()
+        sb2 = np.where(sb == 255, 127, sb).astype(np.uint8)
+        want, bound = R.product(R.fp8_values(q, s), R.mx_values(qb, sb2))
+        keep = np.arange(N) != 200 if step == 2 else np.ones(N, bool)
+        R.assert_product(got[:, keep], want[:, keep], bound[:, keep], False)

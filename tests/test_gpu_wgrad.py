@@ -106,3 +106,18 @@ def test_binding_refuses():
         m.fp8_matmul_tokblk(q, s, q, s, off.int(), 128, 128)
     with pytest.raises(m.Fp4Error):
         m.fp8_matmul_tokblk(q, s, q, s, off, 128, 128, out_dtype=torch.float16)
+
+
+def test_zero_blocks_and_far_apart_scales():
+    m = need_gpu()
+    rng = np.random.default_rng(9)
+    counts = [200, 300]
+    off = R.offsets_of(counts)
+    qa, sa = R.random_columns(rng, off, 128)
+    qb, sb = R.random_columns(rng, off, 256)
+    at = R.column_scale_start(off, 128)
+    qa[3 * 200:4 * 200] = 0
+    sa[at[0] + 6:at[0] + 8] = 2.0 ** -127                # a channel of zeros
+    check(m, rng, counts, 128, 256, "f32", [(qa, sa), (qb, sb)])
+    sa[at[1] + 30] = 2.0 ** 102                          # outside the window; products stay below 2^125
+    check(m, rng, counts, 128, 256, "f32", [(qa, sa), (qb, sb)])

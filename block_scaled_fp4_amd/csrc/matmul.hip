@@ -401,11 +401,59 @@ void launch_tiles(ProductArgs p, int out_dtype, hipStream_t st) {
     launch_1d(product_tiles_kernel<FN, FM, false>, blocks, 256, st, p);
 }
 
+// What the rare path of a tile needs, from the tile's first rows.
+struct Fp8TileView {
+  const uint8_t* x;
+  const float* xs;
+  const uint8_t *w, *ws;
+  int k, xrows, wrows;
+};
+// Whether some scale outside the bf16 window has codes to scale.
+__device__ __attribute__((noinline)) bool scales_need_care(Fp8TileView v) {
+  bool bad = false;
+#pragma unroll 1
+  for (int i = 0; i < v.k >> 5; ++i) {
+    LaneStep<false> lw;
+    LaneStep<true> lx;
+    load_lane<false, false>(v.w, v.ws, min((int)threadIdx.x % kBN, v.wrows - 1), v.k, i >> 2, i & 3, lw);
+    load_lane<true, false>(v.x, v.xs, min((int)threadIdx.x % 128, v.xrows - 1), v.k, i >> 2, i & 3, lx);
+    bad |= !scale_fits(lw) || !scale_fits(lx);
+  }
+  return bad;
+}
+// A wave's 128 x 64 of a tile, 16 x 16 at a time straight from memory, for scales
+// of any range.  Out of line, like the above, so that it costs the common path no
+// registers.
+template <bool BF16>
+__device__ __attribute__((noinline)) void rare_quarter(Fp8TileView v, int mw, int nw, void* out,
+                                                       int64_t out_row, int n_cols, int out_col,
+                                                       const float* row_scale) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i) {
+    const int m = mw + (i >> 3) * 16, n = nw + (i & 7) * 16;
+    LaneStep<false> lw[1];
+    LaneStep<true> lx[1];
+    f32x4 c[1][1] = {};
+#pragma unroll 1
+    for (int s = 0; s < v.k >> 7; ++s) {
+      load_lane<false, false>(v.w, v.ws, min(n + r, v.wrows - 1), v.k, s, g, lw[0]);
+      load_lane<true, false>(v.x, v.xs, min(m + r, v.xrows - 1), v.k, s, g, lx[0]);
+      mfma_bf16_step(lw, lx, c);
+    }
+    if (m + r < v.xrows) {
+      if (row_scale) c[0][0] *= row_scale[out_row + m + r];
+      store_out4<BF16>(out, out_row + m + r, n_cols, out_col + n + 4 * g, c[0][0]);
+    }
+  }
+}
+
 // FP8 rows by MXFP4, see bf16_tile.
+constexpr int kBM = 128;
 template <bool BF16>
 __global__ __launch_bounds__(256, 2) void product_fp8_tiles_kernel(ProductArgs p, int64_t blk0) {
   __shared__ __align__(16) union {
-    Bf16Shared<false> t;
+    Bf16Shared<false, 2> t;
     uint8_t out[4][quarter_bytes<4, BF16>()];
   } sh;
   const int64_t blk = (int64_t)blockIdx.x + blk0;
@@ -420,51 +468,28 @@ __global__ __launch_bounds__(256, 2) void product_fp8_tiles_kernel(ProductArgs p
   const uint8_t* ws = p.w_scales + ((int64_t)e * p.n + n0) * ksb;
   const uint8_t* x = p.a + (int64_t)row0 * p.k;
   const float* xs = static_cast<const float*>(p.a_scales) + (int64_t)row0 * kx;
+  uint32_t wo[4], xo[4];
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    wo[i] = (uint32_t)min((tid >> 2) + 64 * i, wrows - 1) * (uint32_t)kb + (tid & 3) * 16;
+    xo[i] = (uint32_t)min((tid >> 3) + 32 * i, xrows - 1) * (uint32_t)p.k + (tid & 7) * 16;
+  }
   f32x16 acc[4][2] = {};
-  const bool odd = bf16_tile<false>(
+  const bool odd = bf16_tile<false, 2>(
       sh.t, kx, kx,
-      [&](auto, int s, int row, int c) {
-        return *reinterpret_cast<const i32x4*>(w + (int64_t)min(row, wrows - 1) * kb + s * 64 + c * 16);
-      },
-      [&](auto, int s, int row, int c) {
-        return *reinterpret_cast<const i32x4*>(x + (int64_t)min(row, xrows - 1) * p.k + s * 128 + c * 16);
-      },
-      [&](auto, int s, int row) {
+      [&](int s, int i) { return *reinterpret_cast<const i32x4*>(w + s * 64 + wo[i]); },
+      [&](int s, int i) { return *reinterpret_cast<const i32x4*>(x + s * 128 + xo[i]); },
+      [](int, int, i32x4&) {},
+      [&](int s, int row) {
         return *reinterpret_cast<const uint32_t*>(ws + (int64_t)min(row, wrows - 1) * ksb + s * 4);
       },
       [&](int s, int row) { return e8m0_of(xs[(int64_t)min(row, xrows - 1) * kx + s]); }, acc);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m0 = row0 + (wave >> 1) * 64, nw = n0 + (wave & 1) * 128;
-  const auto slow = [&]() {   // whether a scale outside the window has codes to scale
-    bool bad = false;
-    const int wr = min((int)threadIdx.x, wrows - 1), xr = min((int)threadIdx.x % kBM, xrows - 1);
-    for (int i = 0; i < 4 * kx; ++i) {
-      LaneStep<false> lw;
-      LaneStep<true> lx;
-      load_lane<false, false>(w, ws, wr, p.k, i >> 2, i & 3, lw);
-      load_lane<true, false>(x, xs, xr, p.k, i >> 2, i & 3, lx);
-      bad |= !scale_fits(lw) || !scale_fits(lx);
-    }
-    return bad;
-  };
-  if (__syncthreads_or(odd) && __syncthreads_or(slow())) {
-    // rare: 16 x 16 at a time, straight from memory, with every scale's range
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    for (int i = 0; i < 32; ++i) {
-      const int m = m0 + (i >> 3) * 16, n = nw + (i & 7) * 16;
-      LaneStep<false> lw[1];
-      LaneStep<true> lx[1];
-      f32x4 c[1][1] = {};
-      for (int s = 0; s < kx; ++s) {
-        load_lane<false, false>(w, ws, min(n + r, p.n - 1) - n0, p.k, s, g, lw[0]);
-        load_lane<true, false>(x, xs, min(m + r, row_end - 1) - row0, p.k, s, g, lx[0]);
-        mfma_bf16_step(lw, lx, c);
-      }
-      if (m + r < row_end) {
-        if (p.a_row_scale) c[0][0] *= p.a_row_scale[m + r];
-        store_out4<BF16>(p.out, m + r, p.n, n + 4 * g, c[0][0]);
-      }
-    }
+  const Fp8TileView view = {x, xs, w, ws, p.k, xrows, wrows};
+  if (__syncthreads_or(odd) && __syncthreads_or(scales_need_care(view))) {
+    rare_quarter<BF16>(view, m0 - row0, nw - n0, p.out, row0, p.n, n0, p.a_row_scale);
     return;
   }
   store_quarter<4, 2, BF16>(acc, sh.out[wave], p.out, m0, row_end, p.n, nw, p.a_row_scale);

@@ -335,96 +335,117 @@ __device__ __forceinline__ void store_quarter(const f32x16 (&acc)[FN][FM], uint8
 }
 
 // ------------------------------------------------ tiles of bf16 products
-// The E4M3 products at size: one workgroup of four waves owns 256 rows of
-// operand A (the output's columns) by 128 of operand B, each wave 128 x 64 of
+// The E4M3 products at size: one workgroup of 2 WM waves owns 256 rows of
+// operand A (the output's columns) by 64 WM of operand B, each wave 128 x 64 of
 // them in 32 x 32 x 16 instructions.  A stage is 128 k.  Codes are staged
 // through registers into LDS as they are, two stages in turn with one barrier
-// each, and become bf16 values on their way to the instructions.
+// each, and become bf16 values on their way to the instructions; each wave
+// converts 12 operand rows' worth for 64 instructions' time.
 //
 // E4M3 rows are 8 chunks of 16 bytes, chunk c at position c ^ (row % 8); E2M1
 // rows are 4 chunks, c at c ^ (row / 2 % 4): eight consecutive rows then touch
-// every bank once.  Scales lie beside as bytes, one a row (E4M3, one block of
-// 128) or four (E2M1).
-constexpr int kBN = 256, kBM = 128;
+// every bank once.  Scales lie beside for 8 stages at a time, one byte a row and
+// stage (E4M3, one block of 128) or four (E2M1): a stage's own few bytes of
+// each row would cost as many cache lines as its codes.
+constexpr int kBN = 256;
 
-template <bool A8>
+template <bool A8, int WM>
 struct Bf16Shared {
   static constexpr int kA = A8 ? 128 : 64;   // bytes of a row of A
+  static constexpr int kBM = 64 * WM;
   uint8_t a[2][kBN * kA];
   uint8_t b[2][kBM * 128];
-  uint8_t as[2][kBN * (A8 ? 1 : 4)];
-  uint8_t bs[2][kBM];
+  uint8_t as[8][kBN * (A8 ? 1 : 4)];
+  uint8_t bs[8][kBM];
 };
 
-template <bool F8>
-__device__ __forceinline__ int chunk_at(int row, int c) {
-  return F8 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-}
-
-// load_a(s, row, chunk), load_b: 16 bytes of stage s; scale_a(s, row): its four
-// bytes (E2M1) or one (E4M3), scale_b: one.  mid: the stages whose loads need
-// no care at the end of K.  Returns whether some scale this thread loaded was
-// outside the bf16 window.
-template <bool A8, typename LA, typename LB, typename SA, typename SB>
-__device__ __forceinline__ bool bf16_tile(Bf16Shared<A8>& sh, int stages, int full_stages, LA load_a,
-                                          LB load_b, SA scale_a, SB scale_b, f32x16 (&acc)[4][2]) {
-  constexpr int kPerA = Bf16Shared<A8>::kA / 16, kLA = kBN * kPerA / 256, kLB = kBM * 8 / 256;
+// load_a(s, i), load_b: a thread's i-th 16 bytes of stage s, chunk tid % C of
+// row tid / C + i (threads / C), C chunks a row; from stage full_stages on,
+// cut(s, chunk, v) makes of them what counts, once they are there.  scale_a(s, row): the row's word of four bytes (E2M1) or its byte
+// (E4M3), scale_b(s, row): its byte.  Returns whether some scale that this
+// thread loaded was outside the window.
+template <bool A8, int WM, typename LA, typename LB, typename CUT, typename SA, typename SB>
+__device__ __forceinline__ bool bf16_tile(Bf16Shared<A8, WM>& sh, int stages, int full_stages,
+                                          LA load_a, LB load_b, CUT cut, SA scale_a, SB scale_b,
+                                          f32x16 (&acc)[4][2]) {
+  constexpr int T = 128 * WM, kBM = 64 * WM;
+  constexpr int kPerA = Bf16Shared<A8, WM>::kA / 16, kLA = kBN * kPerA / T, kLB = kBM * 8 / T;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave & 1, wm = wave >> 1, r = lane & 31, g = lane >> 5;
   i32x4 ra[kLA], rb[kLB];
-  uint32_t sa = 0, sb = 0;
   bool odd_scale = false;
-  auto fetch = [&](auto full, int s) {
+  auto fetch = [&](int s) {
 #pragma unroll
-    for (int i = 0; i < kLA; ++i) ra[i] = load_a(full, s, (i * 256 + tid) / kPerA, tid % kPerA);
+    for (int i = 0; i < kLA; ++i) ra[i] = load_a(s, i);
 #pragma unroll
-    for (int i = 0; i < kLB; ++i) rb[i] = load_b(full, s, (i * 256 + tid) / 8, tid % 8);
-    sa = scale_a(full, s, tid);
-    sb = scale_b(s, tid % kBM);
+    for (int i = 0; i < kLB; ++i) rb[i] = load_b(s, i);
   };
-  auto put = [&](int b) {
+  // T / C is a multiple of 8, so a thread's rows share their place in the pattern
+  const int put8 = (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4);
+  const int put4 = (tid >> 2) * 64 + (((tid & 3) ^ ((tid >> 3) & 3)) << 4);
+  auto put = [&](int s) {
+    const int b = s & 1;
+    if (s >= full_stages) {
+#pragma unroll
+      for (int i = 0; i < kLA; ++i) cut(s, tid % kPerA, ra[i]);
+#pragma unroll
+      for (int i = 0; i < kLB; ++i) cut(s, tid % 8, rb[i]);
+    }
 #pragma unroll
     for (int i = 0; i < kLA; ++i)
-      *reinterpret_cast<i32x4*>(&sh.a[b][chunk_at<A8>((i * 256 + tid) / kPerA, tid % kPerA)]) = ra[i];
+      *reinterpret_cast<i32x4*>(&sh.a[b][(A8 ? put8 : put4) + i * T * 16]) = ra[i];
 #pragma unroll
-    for (int i = 0; i < kLB; ++i)
-      *reinterpret_cast<i32x4*>(&sh.b[b][chunk_at<true>((i * 256 + tid) / 8, tid % 8)]) = rb[i];
-    if constexpr (A8) {
-      sh.as[b][tid] = (uint8_t)sa;
-      odd_scale |= !scale_in_window((int)sa);
-    } else {
-      reinterpret_cast<uint32_t*>(sh.as[b])[tid] = sa;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) odd_scale |= !scale_in_window((int)((sa >> (8 * j)) & 0xFFu));
-    }
-    sh.bs[b][tid % kBM] = (uint8_t)sb;
-    odd_scale |= !scale_in_window((int)sb);
+    for (int i = 0; i < kLB; ++i) *reinterpret_cast<i32x4*>(&sh.b[b][put8 + i * T * 16]) = rb[i];
   };
-  auto compute = [&](int b) {
+  // the scales of stages 8 grp .. 8 grp + 7
+  auto put_scales = [&](int grp) {
+    uint32_t va[8], vb[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int s = min(8 * grp + j, stages - 1);
+      va[j] = scale_a(s, tid % kBN);
+      vb[j] = scale_b(s, tid % kBM);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (A8) {
+        sh.as[j][tid % kBN] = (uint8_t)va[j];
+        odd_scale |= !scale_in_window((int)va[j]);
+      } else {
+        reinterpret_cast<uint32_t*>(sh.as[j])[tid % kBN] = va[j];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) odd_scale |= !scale_in_window((int)((va[j] >> (8 * q)) & 0xFFu));
+      }
+      sh.bs[j][tid % kBM] = (uint8_t)vb[j];
+      odd_scale |= !scale_in_window((int)vb[j]);
+    }
+  };
+  const int rb0 = (wm * 64 + r) * 128, ra0 = (wn * 128 + r) * Bf16Shared<A8, WM>::kA;
+  auto compute = [&](int s) {
+    const int b = s & 1, sj = s & 7;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
+      const int c0 = ((4 * ks + 2 * g) ^ (r & 7)) << 4, c1 = c0 ^ 16, c4 = ((2 * ks + g) ^ ((r >> 1) & 3)) << 4;
       bf16x8_t y[2][4];
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        const int row = (wm * 2 + f) * 32 + r;
         Frag<true> v;
-        v.lo = *reinterpret_cast<const i32x4*>(&sh.b[b][chunk_at<true>(row, 4 * ks + 2 * g)]);
-        v.hi = *reinterpret_cast<const i32x4*>(&sh.b[b][chunk_at<true>(row, 4 * ks + 2 * g + 1)]);
-        const float sc = scale_of(sh.bs[b][row]);
+        v.lo = *reinterpret_cast<const i32x4*>(&sh.b[b][rb0 + f * 32 * 128 + c0]);
+        v.hi = *reinterpret_cast<const i32x4*>(&sh.b[b][rb0 + f * 32 * 128 + c1]);
+        const float sc = scale_of(sh.bs[sj][wm * 64 + f * 32 + r]);
         unrolled<4>([&](auto q) { y[f][q] = bf16_of<decltype(q)::value>(v, sc); });
       }
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
-        const int row = (wn * 4 + f) * 32 + r;
         Frag<A8> v;
         float sc;
         if constexpr (A8) {
-          v.lo = *reinterpret_cast<const i32x4*>(&sh.a[b][chunk_at<true>(row, 4 * ks + 2 * g)]);
-          v.hi = *reinterpret_cast<const i32x4*>(&sh.a[b][chunk_at<true>(row, 4 * ks + 2 * g + 1)]);
-          sc = scale_of(sh.as[b][row]);
+          v.lo = *reinterpret_cast<const i32x4*>(&sh.a[b][ra0 + f * 32 * 128 + c0]);
+          v.hi = *reinterpret_cast<const i32x4*>(&sh.a[b][ra0 + f * 32 * 128 + c1]);
+          sc = scale_of(sh.as[sj][wn * 128 + f * 32 + r]);
         } else {
-          v.lo = *reinterpret_cast<const i32x4*>(&sh.a[b][chunk_at<false>(row, 2 * ks + g)]);
-          sc = scale_of(sh.as[b][row * 4 + 2 * ks + g]);
+          v.lo = *reinterpret_cast<const i32x4*>(&sh.a[b][ra0 + f * 32 * 64 + c4]);
+          sc = scale_of(sh.as[sj][(wn * 128 + f * 32 + r) * 4 + 2 * ks + g]);
         }
         unrolled<4>([&](auto q) {
           const bf16x8_t x = bf16_of<decltype(q)::value>(v, sc);
@@ -436,21 +457,25 @@ __device__ __forceinline__ bool bf16_tile(Bf16Shared<A8>& sh, int stages, int fu
     }
   };
   if (stages == 0) return false;
-  fetch(std::false_type(), 0);
+  fetch(0);
+  put_scales(0);
   put(0);
   __syncthreads();
-  int s = 0;
-  for (; s + 1 < full_stages; ++s) {
-    fetch(std::true_type(), s + 1);
-    compute(s & 1);
-    put((s + 1) & 1);
+  for (int s = 0; s < stages; ++s) {
+    fetch(min(s + 1, stages - 1));
+    compute(s);
+    // the products stay before what follows: sums left for later would be
+    // moved past the branches to the end of the loop
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(acc[f][j]));
+    put(s + 1);
     __syncthreads();
-  }
-  for (; s < stages; ++s) {
-    if (s + 1 < stages) fetch(std::false_type(), s + 1);
-    compute(s & 1);
-    if (s + 1 < stages) put((s + 1) & 1);
-    __syncthreads();
+    if ((s & 7) == 7) {   // past the barrier all have read these eight
+      put_scales(s / 8 + 1);
+      __syncthreads();
+    }
   }
   return odd_scale;
 }

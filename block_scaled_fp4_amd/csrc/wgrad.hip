@@ -19,27 +19,34 @@ struct WgradArgs {
   int m_tiles, n_tiles;
 };
 
-// 32 tokens t .. t+31 of a channel at any byte alignment; tokens past the
-// shard's end count as zero and are not read.
-__device__ __forceinline__ Frag<true> load_tokens(const uint8_t* ch, int t, int count) {
-  Frag<true> f;
-  if (t + 32 <= count) {
-    memcpy(&f.lo, ch + t, 16);
-    memcpy(&f.hi, ch + t + 16, 16);
-  } else {
-    int w[8];
+// 16 tokens from t of a channel of `count`, at any byte alignment.  Tokens past
+// the end are not read: the load ends at the last token, and cut_tokens16
+// shifts it down, so that they count as zero.
+__device__ __forceinline__ i32x4 load_tokens16(const uint8_t* ch, uint32_t t) {
+  i32x4 v;
+  memcpy(&v, ch + t, 16);
+  return v;
+}
+__device__ __forceinline__ void cut_tokens16(int t, int count, i32x4& v) {   // count >= 16
+  const int drop = min(t - min(t, count - 16), 16) * 8, d = drop & 63;
+  uint64_t q[2];
+  memcpy(q, &v, 16);
+  const uint64_t hi = q[1] >> d, lo = d ? (q[0] >> d) | (q[1] << (64 - d)) : q[0];
+  const uint64_t l = drop < 64 ? lo : (drop < 128 ? hi : 0), h = drop < 64 ? hi : 0;
+  v = i32x4{(int)l, (int)(l >> 32), (int)h, (int)(h >> 32)};
+}
+// The same for any count, byte by byte.
+__device__ __forceinline__ i32x4 load_few_tokens16(const uint8_t* ch, int t, int count) {
+  uint64_t q[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t v = 0;
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        if (t + 4 * i + b < count) v |= (uint32_t)ch[t + 4 * i + b] << (8 * b);
-      w[i] = (int)v;
-    }
-    f.lo = i32x4{w[0], w[1], w[2], w[3]};
-    f.hi = i32x4{w[4], w[5], w[6], w[7]};
+  for (int h = 0; h < 2; ++h) {
+    uint64_t w = 0;
+    const int n = min(count - t - 8 * h, 8);
+#pragma unroll 1
+    for (int b = 0; b < n; ++b) w |= (uint64_t)ch[t + 8 * h + b] << (8 * b);
+    q[h] = w;
   }
-  return f;
+  return i32x4{(int)q[0], (int)(q[0] >> 32), (int)q[1], (int)(q[1] >> 32)};
 }
 
 struct LaneTokens {
@@ -47,32 +54,62 @@ struct LaneTokens {
   int s;
 };
 
-// 16 tokens from t; FULL: all inside the shard.
-template <bool FULL>
-__device__ __forceinline__ i32x4 load_tokens16(const uint8_t* ch, int t, int count) {
-  i32x4 v;
-  if (FULL || t + 16 <= count) {
-    memcpy(&v, ch + t, 16);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t w = 0;
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        if (t + 4 * i + b < count) w |= (uint32_t)ch[t + 4 * i + b] << (8 * b);
-      v[i] = (int)w;
-    }
+// What the rare path of a tile needs of its shard: from channel 0 of the tile.
+struct TileView {
+  const uint8_t *a, *b;
+  const float *as, *bs;
+  int cnt, blocks, mrows, nrows;
+};
+__device__ __forceinline__ void lane_tokens(const uint8_t* ch, const float* sc, int row, int cnt,
+                                            int blocks, int s, int g, LaneTokens& l) {
+  l.v.lo = load_few_tokens16(ch + (int64_t)row * cnt, 128 * s + 32 * g, cnt);
+  l.v.hi = load_few_tokens16(ch + (int64_t)row * cnt, 128 * s + 32 * g + 16, cnt);
+  l.s = (int)e8m0_of(sc[(int64_t)row * blocks + s]);
+}
+// Whether some scale outside the bf16 window has codes to scale.
+template <int BM>
+__device__ __attribute__((noinline)) bool scales_need_care(TileView v) {
+  bool bad = false;
+#pragma unroll 1
+  for (int i = 0; i < 4 * v.blocks; ++i) {
+    LaneTokens lb, la;
+    lane_tokens(v.b, v.bs, min((int)threadIdx.x % kBN, v.nrows - 1), v.cnt, v.blocks, i >> 2, i & 3, lb);
+    lane_tokens(v.a, v.as, min((int)threadIdx.x % BM, v.mrows - 1), v.cnt, v.blocks, i >> 2, i & 3, la);
+    bad |= !scale_fits(lb) || !scale_fits(la);
   }
-  return v;
+  return bad;
+}
+// A wave's 128 x 64 of a tile at channels mw, nw of it, 16 x 16 at a time
+// straight from memory, for scales of any range and any number of tokens.  Out
+// of line, like the above, so that it costs the common path no registers.
+template <bool BF16>
+__device__ __attribute__((noinline)) void rare_quarter(TileView v, int mw, int nw, void* out,
+                                                       int64_t out_row, int n_cols, int out_col) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  if (nw >= v.nrows || mw >= v.mrows) return;   // sides are multiples of 128
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i) {
+    const int m = mw + (i >> 3) * 16, n = nw + (i & 7) * 16;
+    LaneTokens lb[1], la[1];
+    f32x4 c[1][1] = {};
+#pragma unroll 1
+    for (int s = 0; s < v.blocks; ++s) {
+      lane_tokens(v.b, v.bs, n + r, v.cnt, v.blocks, s, g, lb[0]);
+      lane_tokens(v.a, v.as, m + r, v.cnt, v.blocks, s, g, la[0]);
+      mfma_bf16_step(lb, la, c);
+    }
+    store_out4<BF16>(out, out_row + m + r, n_cols, out_col + n + 4 * g, c[0][0]);
+  }
 }
 
 // See bf16_tile: channels of b are its operand A (consecutive columns of the
 // output), channels of a its operand B, tokens its k.
-template <bool BF16>
-__global__ __launch_bounds__(256, 1) void wgrad_tiles_kernel(WgradArgs p, int64_t blk0) {
+template <int WM, bool BF16>
+__global__ __launch_bounds__(128 * WM, 1) void wgrad_tiles_kernel(WgradArgs p, int64_t blk0) {
+  constexpr int kBM = 64 * WM;
   __shared__ __align__(16) union {
-    Bf16Shared<true> t;
-    uint8_t out[4][quarter_bytes<4, BF16>()];
+    Bf16Shared<true, WM> t;
+    uint8_t out[2 * WM][quarter_bytes<4, BF16>()];
   } sh;
   const int64_t blk = (int64_t)blockIdx.x + blk0;
   const int nt = (int)(blk % p.n_tiles), mt = (int)((blk / p.n_tiles) % p.m_tiles);
@@ -81,57 +118,47 @@ __global__ __launch_bounds__(256, 1) void wgrad_tiles_kernel(WgradArgs p, int64_
   shard_bounds(p.offsets, e, p.tokens, lo, hi);
   const int cnt = hi - lo, blocks = (cnt + 127) >> 7;
   const int64_t sblk = ((int64_t)lo + 127) / 128 + e;
-  const int m0 = mt * kBM, n0 = nt * kBN, nrows = p.n - n0;
+  const int m0 = mt * kBM, n0 = nt * kBN, nrows = p.n - n0, mrows = p.m - m0;
   const uint8_t* a = p.a + (int64_t)p.m * lo + (int64_t)m0 * cnt;
   const uint8_t* b = p.b + (int64_t)p.n * lo + (int64_t)n0 * cnt;
   const float* as = p.a_scales + sblk * p.m + (int64_t)m0 * blocks;
   const float* bs = p.b_scales + sblk * p.n + (int64_t)n0 * blocks;
-  f32x16 acc[4][2] = {};
-  const bool odd = bf16_tile<true>(
-      sh.t, blocks, cnt >> 7,
-      [&](auto full, int s, int row, int c) {
-        return load_tokens16<decltype(full)::value>(b + (int64_t)min(row, nrows - 1) * cnt, s * 128 + c * 16, cnt);
-      },
-      [&](auto full, int s, int row, int c) {
-        return load_tokens16<decltype(full)::value>(a + (int64_t)row * cnt, s * 128 + c * 16, cnt);
-      },
-      [&](auto, int s, int row) { return e8m0_of(bs[(int64_t)min(row, nrows - 1) * blocks + s]); },
-      [&](int s, int row) { return e8m0_of(as[(int64_t)row * blocks + s]); }, acc);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int mw = m0 + (wave >> 1) * 64, nw = n0 + (wave & 1) * 128;
   const int64_t orow = (int64_t)e * p.m;
-  auto lane_tokens = [&](const uint8_t* ch, const float* sc, int row, int s, int g, LaneTokens& l) {
-    l.v = load_tokens(ch + (int64_t)row * cnt, 128 * s + 32 * g, cnt);
-    l.s = (int)e8m0_of(sc[(int64_t)row * blocks + s]);
-  };
-  const auto slow = [&]() {   // whether a scale outside the window has codes to scale
-    bool bad = false;
-    for (int i = 0; i < 4 * blocks; ++i) {
-      LaneTokens lb, la;
-      lane_tokens(b, bs, min((int)threadIdx.x, nrows - 1), i >> 2, i & 3, lb);
-      lane_tokens(a, as, threadIdx.x % kBM, i >> 2, i & 3, la);
-      bad |= !scale_fits(lb) || !scale_fits(la);
-    }
-    return bad;
-  };
-  if (__syncthreads_or(odd) && __syncthreads_or(slow())) {
-    // rare: 16 x 16 at a time, straight from memory, with every scale's range
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    if (nw >= p.n) return;
-    for (int i = 0; i < 32; ++i) {
-      const int m = mw + (i >> 3) * 16, n = nw + (i & 7) * 16;
-      LaneTokens lb[1], la[1];
-      f32x4 c[1][1] = {};
-      for (int s = 0; s < blocks; ++s) {
-        lane_tokens(b, bs, n - n0 + r, s, g, lb[0]);
-        lane_tokens(a, as, m - m0 + r, s, g, la[0]);
-        mfma_bf16_step(lb, la, c);
-      }
-      store_out4<BF16>(p.out, orow + m + r, p.n, n + 4 * g, c[0][0]);
-    }
+  const TileView view = {a, b, as, bs, cnt, blocks, mrows, nrows};
+  f32x16 acc[4][2] = {};
+  // rare cases go 16 x 16 at a time, straight from memory: scales outside the
+  // bf16 window over codes, and shards too short for a load of 16 tokens
+  bool rare = cnt > 0 && cnt < 16;
+  // a thread's rows are 16 WM apart; with only 128 rows left on a side, those
+  // past them are the first again
+  const int ch = (threadIdx.x & 7) * 16;
+  const uint32_t row_at = (threadIdx.x >> 3) * (uint32_t)cnt;
+  const int64_t step = (int64_t)(16 * WM) * cnt;
+  const int ia = nrows >= kBN ? 15 : 128 / (16 * WM) - 1, ib = mrows >= kBM ? 15 : 128 / (16 * WM) - 1;
+  if (!rare) {
+    const bool odd = bf16_tile<true, WM>(
+        sh.t, blocks, cnt >> 7,
+        [&](int s, int i) { return load_tokens16(b + (i & ia) * step, row_at + (uint32_t)min(s * 128 + ch, cnt - 16)); },
+        [&](int s, int i) { return load_tokens16(a + (i & ib) * step, row_at + (uint32_t)min(s * 128 + ch, cnt - 16)); },
+        [&](int s, int c, i32x4& v) { cut_tokens16(s * 128 + c * 16, cnt, v); },
+        [&](int s, int row) { return e8m0_of(bs[(int64_t)min(row, nrows - 1) * blocks + s]); },
+        [&](int s, int row) { return e8m0_of(as[(int64_t)min(row, mrows - 1) * blocks + s]); }, acc);
+    rare = __syncthreads_or(odd) && __syncthreads_or(scales_need_care<kBM>(view));
+  }
+  if (rare) {
+    rare_quarter<BF16>(view, mw - m0, nw - n0, p.out, orow + m0, p.n, n0);
     return;
   }
   store_quarter<4, 2, BF16>(acc, sh.out[wave], p.out, orow + mw, orow + p.m, p.n, nw, nullptr);
+}
+
+template <int WM, bool BF16>
+void launch_wgrad(WgradArgs p, int64_t experts, hipStream_t st) {
+  p.m_tiles = (p.m + 64 * WM - 1) / (64 * WM);
+  p.n_tiles = (p.n + kBN - 1) / kBN;
+  launch_1d(wgrad_tiles_kernel<WM, BF16>, experts * p.m_tiles * p.n_tiles, 128 * WM, st, p);
 }
 
 }  // namespace
@@ -148,7 +175,7 @@ extern "C" int fp8_matmul_tokblk(const uint8_t* a, const float* a_scales, const 
   if (!osz) return FP4_EDTYPE;
   const int64_t T = total_tokens, E = num_experts;
   if (T < 0 || M < 0 || N < 0 || M % 128 || N % 128) return FP4_ESHAPE;
-  if (T >= (int64_t(1) << 26) || M >= (int64_t(1) << 21) || N >= (int64_t(1) << 21) ||
+  if (T >= (int64_t(1) << 24) || M >= (int64_t(1) << 21) || N >= (int64_t(1) << 21) ||
       E >= (int64_t(1) << 23))
     return FP4_ESHAPE;
   int64_t n_a, n_b, n_mn, n_out;
@@ -166,14 +193,13 @@ extern "C" int fp8_matmul_tokblk(const uint8_t* a, const float* a_scales, const 
   const int64_t inn[5] = {n_a, T ? M * blocks * 4 : 0, n_b, T ? N * blocks * 4 : 0, (E + 1) * 8};
   for (int i = 0; i < 5; ++i)
     if (overlaps(out, n_out * osz, ins[i], inn[i])) return FP4_EOVERLAP;
-  WgradArgs p = {a, a_scales, b, b_scales, token_offsets, out, (int)T, (int)M, (int)N,
-                 (int)(M / kBM), (int)((N + kBN - 1) / kBN)};
+  WgradArgs p = {a, a_scales, b, b_scales, token_offsets, out, (int)T, (int)M, (int)N, 0, 0};
   clear_stale_error();
   hipStream_t st = as_stream(stream);
-  const int64_t grid = E * p.m_tiles * p.n_tiles;
-  if (out_dtype == FP4_DTYPE_BF16)
-    launch_1d(wgrad_tiles_kernel<true>, grid, 256, st, p);
+  const bool bf16 = out_dtype == FP4_DTYPE_BF16;
+  if (E * ((M + 255) / 256) * ((N + 255) / 256) >= 512)
+    bf16 ? launch_wgrad<4, true>(p, E, st) : launch_wgrad<4, false>(p, E, st);
   else
-    launch_1d(wgrad_tiles_kernel<false>, grid, 256, st, p);
+    bf16 ? launch_wgrad<2, true>(p, E, st) : launch_wgrad<2, false>(p, E, st);
   return launch_status();
 }

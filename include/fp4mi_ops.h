@@ -84,7 +84,7 @@ int mxfp4_matmul_grouped(const void* a, int a_fmt, const void* a_scales, const f
  *  a, b           bytes [T * M], [T * N], 4-byte aligned
  *  a_scales, b_scales  fp32 [M (ceil(T/128) + E)], [N (ceil(T/128) + E)],
  *                 4-byte aligned
- *  token_offsets, num_experts, total_tokens  as mxfp4_matmul_grouped
+ *  token_offsets, num_experts  as mxfp4_matmul_grouped;  0 <= T < 2^24
  *  M, N           >= 0, below 2^21, % 128 == 0
  *  out            [E, M, N] in out_dtype, 16-byte aligned; must not overlap an input
  */

@@ -121,3 +121,11 @@ def test_zero_blocks_and_far_apart_scales():
     check(m, rng, counts, 128, 256, "f32", [(qa, sa), (qb, sb)])
     sa[at[1] + 30] = 2.0 ** 102                          # outside the window; products stay below 2^125
     check(m, rng, counts, 128, 256, "f32", [(qa, sa), (qb, sb)])
+
+
+@pytest.mark.parametrize("counts,M,N", [([130, 0, 300, 65] * 8, 1024, 1152), ([1100, 5], 4096, 4224)])
+def test_larger_outputs(counts, M, N):
+    """Enough tiles for the larger of the two tile shapes, with a half tile at
+    the end of either side."""
+    m = need_gpu()
+    check(m, np.random.default_rng(M), counts, M - 128, N, "f32" if M < 2000 else "bf16")

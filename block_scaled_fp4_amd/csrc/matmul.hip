@@ -42,6 +42,35 @@ __device__ __forceinline__ void load_lane(const uint8_t* base, const void* scale
   }
 }
 
+// 4 scale bytes of a row of `bytes` >= 4 from byte `at`.  Past the row's end
+// stand other bytes of the row: the codes there count as zero, and a NaN scale
+// among them makes the same outputs NaN by itself.  FULL: there are none.
+template <bool FULL>
+__device__ __forceinline__ uint32_t load_scales4(const uint8_t* row, int at, int bytes) {
+  const int have = FULL ? at : min(at, bytes - 4);
+  uint32_t w;
+  memcpy(&w, row + have, 4);
+  return FULL ? w : w >> (8 * min(at - have, 3));
+}
+
+// The U words of scale bytes (four blocks of 32, or one fp32 scale, a word) of
+// steps st .. st + U - 1 of a row, in one load where the row has them all.
+template <int U>
+__device__ __forceinline__ void load_scale_words(const uint8_t* row, int st, int bytes,
+                                                 uint32_t (&v)[U]) {
+  if (4 * (st + U) <= bytes) {
+    memcpy(v, row + 4 * st, 4 * U);
+  } else if (bytes >= 4) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = load_scales4<false>(row, 4 * (st + u), bytes);
+  } else {   // K < 128
+    uint32_t w = 0;
+    for (int i = 0; i < bytes; ++i) w |= (uint32_t)row[i] << (8 * i);
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = w;
+  }
+}
+
 template <bool A8, bool KT, int FN, int FM, int W, int U, bool BF16>
 __global__ __launch_bounds__(64 * W) void product_rows_kernel(ProductArgs p, int64_t blk0) {
   __shared__ f32x4 red[W][FN * FM][64];
@@ -63,43 +92,72 @@ __global__ __launch_bounds__(64 * W) void product_rows_kernel(ProductArgs p, int
 
   f32x4 acc[FN][FM] = {};
   const int steps = (p.k + 127) >> 7;
-  LaneStep<false> wc[U][FN], wx[U][FN];
-  LaneStep<A8> ac[U][FM], ax[U][FM];
-  auto load = [&](int c, LaneStep<false>(&lw)[U][FN], LaneStep<A8>(&la)[U][FM]) {
+  struct Batch {
+    LaneStep<false> w[U][FN];
+    LaneStep<A8> a[U][FM];
+  } even = {}, odd = {};   // in turn, so that no load is waited for before its use
+  // Loads are counted here, not bytes: one instruction takes the scales of U
+  // steps, and with few tokens lanes past the last load nothing.
+  const int kb = p.k >> 1, ksb = p.k >> 5;
+  auto load = [&](int c, Batch& b) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int st = min(c + u, steps - 1);
+    for (int f = 0; f < FN; ++f) {
+      uint32_t sc[U];
+      load_scale_words<U>(ws + (int64_t)wn[f] * ksb, c, ksb, sc);
 #pragma unroll
-      for (int f = 0; f < FN; ++f) load_lane<false, KT>(w, ws, wn[f], p.k, st, g, lw[u][f]);
+      for (int u = 0; u < U; ++u) {
+        const int kk = min(c + u, steps - 1) * 128 + 32 * g;
+        const bool in = !KT || kk < p.k;
+        b.w[u][f].v.lo = *reinterpret_cast<const i32x4*>(w + (int64_t)wn[f] * kb + ((in ? kk : 0) >> 1));
+        if (KT && !in) b.w[u][f].v.lo = i32x4{0, 0, 0, 0};   // past K codes count as zero
+        b.w[u][f].s = (int)((sc[u] >> (8 * g)) & 0xFFu);
+      }
+    }
 #pragma unroll
-      for (int f = 0; f < FM; ++f) load_lane<A8, KT>(p.a, p.a_scales, am[f], p.k, st, g, la[u][f]);
+    for (int f = 0; f < FM; ++f) {
+      if (FM <= 2 && row0 + 16 * f + r >= row_end) continue;
+      uint32_t sc[U];
+      load_scale_words<U>(static_cast<const uint8_t*>(p.a_scales) + (int64_t)am[f] * (A8 ? p.k >> 5 : ksb),
+                          c, ksb, sc);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int kk = min(c + u, steps - 1) * 128 + 32 * g, at = !KT || kk < p.k ? kk : 0;
+        if constexpr (A8) {
+          const i32x4* q = reinterpret_cast<const i32x4*>(p.a + (int64_t)am[f] * p.k + at);
+          b.a[u][f].v.lo = q[0];
+          b.a[u][f].v.hi = q[1];
+          b.a[u][f].s = (int)((sc[u] >> 23) & 0xFFu);
+        } else {
+          b.a[u][f].v.lo = *reinterpret_cast<const i32x4*>(p.a + (int64_t)am[f] * kb + (at >> 1));
+          b.a[u][f].s = (int)((sc[u] >> (8 * g)) & 0xFFu);
+        }
+      }
     }
   };
-  int c = wave * U;
-  if (c < steps) load(c, wc, ac);
-  for (; c < steps; c += W * U) {
-    if (c + W * U < steps) load(c + W * U, wx, ax);
+  auto multiply = [&](int c, const Batch& b) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (c + u >= steps) continue;
       if constexpr (A8) {
-        mfma_bf16_step(wc[u], ac[u], acc);
+        mfma_bf16_step(b.w[u], b.a[u], acc);
       } else {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
           for (int j = 0; j < FM; ++j)
-            acc[i][j] = mfma_scaled<0, 0>(wc[u][i].v, ac[u][j].v, acc[i][j], wc[u][i].s,
-                                                     ac[u][j].s);
+            acc[i][j] = mfma_scaled<0, 0>(b.w[u][i].v, b.a[u][j].v, acc[i][j], b.w[u][i].s, b.a[u][j].s);
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int f = 0; f < FN; ++f) wc[u][f] = wx[u][f];
-#pragma unroll
-      for (int f = 0; f < FM; ++f) ac[u][f] = ax[u][f];
-    }
+  };
+  int c = wave * U;
+  constexpr int S = W * U;
+  if (c < steps) load(c, even);
+  for (; c < steps; c += 2 * S) {
+    if (c + S < steps) load(c + S, odd);
+    multiply(c, even);
+    if (c + S >= steps) break;
+    if (c + 2 * S < steps) load(c + 2 * S, even);
+    multiply(c + S, odd);
   }
 #pragma unroll
   for (int i = 0; i < FN; ++i)
@@ -152,17 +210,6 @@ template <int SA, int SB>
 __device__ __forceinline__ f32x16 mfma_scaled32(i32x4 a, i32x4 b, f32x16 c, int sa, int sb) {
   const i32x8 x = {a.x, a.y, a.z, a.w, 0, 0, 0, 0}, y = {b.x, b.y, b.z, b.w, 0, 0, 0, 0};
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, kE2M1, kE2M1, SA, sa, SB, sb);
-}
-
-// 4 scale bytes of a row of `bytes` >= 4 from byte `at`.  Past the row's end
-// stand other bytes of the row: the codes there count as zero, and a NaN scale
-// among them makes the same outputs NaN by itself.  FULL: there are none.
-template <bool FULL>
-__device__ __forceinline__ uint32_t load_scales4(const uint8_t* row, int at, int bytes) {
-  const int have = FULL ? at : min(at, bytes - 4);
-  uint32_t w;
-  memcpy(&w, row + have, 4);
-  return FULL ? w : w >> (8 * min(at - have, 3));
 }
 
 // Byte j of four words -> word j.
@@ -504,16 +551,33 @@ void launch_fp8_tiles(ProductArgs p, int out_dtype, hipStream_t st) {
     launch_1d(product_fp8_tiles_kernel<false>, blocks, 256, st, p);
 }
 
+// Which kernel.  Up to 16 tokens: 16 x 16 a workgroup, the most workgroups (4096
+// x 7168 by one token: 5.4 us, 7.1 us with 32 x 32).  Then 32 x 32, whose time
+// follows the number of workgroups, until the tiles, whose time hardly depends
+// on it before the card is full, are faster (k = 4096; us, 32 x 32 | tiles):
+//   MXFP4 by workgroups of 32 x 32: 512: 13.5 | 19.5, 1024: 24.4 | 22.6,
+//   2048: 44.8 | 23.0; FP8: 1024: 44.6 | 72, 2048: 87 | 72.
+// Grouped, by tokens per shard (Zipf shards), where weights are read once a row
+// tile: MXFP4 16: 69 | 72, 32: 70 | 53; FP8 32: 69 | 73, 128: 204 | 77.
+// Of the MXFP4 tiles, 256 x 128 keeps more compute units busy and 256 x 256 feeds
+// the matrix cores better: 256 tiles of the first 28.9 | 33.8, 512 55 | 44; with
+// shards under 256 tokens the second's rows stand empty (64 a shard: 55 | 69).
 template <bool A8, bool KT>
 void launch_product(const ProductArgs& p, int out_dtype, hipStream_t st) {
   const int64_t per = p.tokens / p.experts;
-  if constexpr (A8) {
-    if (per >= 128) return launch_fp8_tiles(p, out_dtype, st);
+  const bool grouped = p.offsets != nullptr;
+  const int64_t small = (int64_t)((p.n + 31) / 32) * ((p.tokens + 31) / 32);
+  const bool tiles = p.k >= 128 && (grouped ? per >= (A8 ? 40 : 24) : small > (A8 ? 1600 : 768));
+  if (!tiles) {
+    if (p.tokens <= 16) launch_rows<A8, KT, 1, 1, 8, 4>(p, out_dtype, st);
+    else launch_rows<A8, KT, 2, 2, 8, 2>(p, out_dtype, st);
+  } else if constexpr (A8) {
+    launch_fp8_tiles(p, out_dtype, st);
   } else {
-    if (per >= 512) return launch_tiles<4, 4>(p, out_dtype, st);
-    if (per >= 128) return launch_tiles<4, 2>(p, out_dtype, st);
+    const int64_t wide = (int64_t)((p.n + 255) / 256) * max_row_tiles(p.tokens, p.experts, 128, grouped);
+    if (wide > 256 && (!grouped || per >= 256)) launch_tiles<4, 4>(p, out_dtype, st);
+    else launch_tiles<4, 2>(p, out_dtype, st);
   }
-  launch_rows<A8, KT, 2, 2, 4, 2>(p, out_dtype, st);
 }
 
 // Checks shared by both products; experts == 0 stands for the plain one.

@@ -305,3 +305,21 @@ def test_large_fp8_tiles_with_scales_out_of_window():
         want, bound = R.product(R.fp8_values(q, s), R.mx_values(qb, sb2))
         keep = np.arange(N) != 200 if step == 2 else np.ones(N, bool)
         R.assert_product(got[:, keep], want[:, keep], bound[:, keep], False)
+
+
+@pytest.mark.parametrize("M,N,K,act", [(1000, 1100, 256, "mxfp4"), (1030, 4100, 160, "mxfp4"), (4099, 2050, 224, "mxfp4"),
+                                       (4200, 2100, 1568, "mxfp4"), (1500, 1300, 128, "fp8"), (1700, 1290, 384, "fp8"),
+                                       (900, 1025, 2080, "mxfp4"), (16, 515, 1056, "mxfp4"), (13, 200, 1152, "fp8")])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_every_kernel(M, N, K, act, out):
+    """Shapes on both sides of each choice of kernel, with odd edges and short
+    last steps and stages."""
+    m = need_gpu()
+    check_dense(m, np.random.default_rng(M + K), M, N, K, act, out, M % 2 == 0)
+
+
+@pytest.mark.parametrize("counts,N,K,act", [([300, 0, 20, 700, 1], 260, 288, "mxfp4"), ([1200, 3, 800], 4100, 160, "mxfp4"),
+                                            ([100, 0, 200, 17], 300, 256, "fp8"), ([30] * 9, 100, 1152, "fp8")])
+def test_grouped_kernels(counts, N, K, act):
+    m = need_gpu()
+    check_grouped(m, np.random.default_rng(K), counts, N, K, act, "f32", True)

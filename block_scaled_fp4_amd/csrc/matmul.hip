@@ -525,9 +525,9 @@ __global__ __launch_bounds__(256, 2) void product_fp8_tiles_kernel(ProductArgs p
   f32x16 acc[4][2] = {};
   const bool odd = bf16_tile<false, 2>(
       sh.t, kx, kx,
-      [&](int s, int i) { return *reinterpret_cast<const i32x4*>(w + s * 64 + wo[i]); },
-      [&](int s, int i) { return *reinterpret_cast<const i32x4*>(x + s * 128 + xo[i]); },
-      [](int, int, i32x4&) {},
+      [&](auto, int s, int i) { return *reinterpret_cast<const i32x4*>(w + s * 64 + wo[i]); },
+      [&](auto, int s, int i) { return *reinterpret_cast<const i32x4*>(x + s * 128 + xo[i]); },
+      [](int, int, i32x4&) {}, [](int, int, i32x4&) {},
       [&](int s, int row) {
         return *reinterpret_cast<const uint32_t*>(ws + (int64_t)min(row, wrows - 1) * ksb + s * 4);
       },

@@ -359,14 +359,16 @@ struct Bf16Shared {
   uint8_t bs[8][kBM];
 };
 
-// load_a(s, i), load_b: a thread's i-th 16 bytes of stage s, chunk tid % C of
-// row tid / C + i (threads / C), C chunks a row; from stage full_stages on,
-// cut(s, chunk, v) makes of them what counts, once they are there.  scale_a(s, row): the row's word of four bytes (E2M1) or its byte
+// load_a(first, s, i), load_b: a thread's i-th 16 bytes of stage s (the first
+// stage, where `first` says so), chunk tid % C of row tid / C + i (threads / C),
+// C chunks a row; from stage full_stages on, cut_a(s, i, v), cut_b make of them
+// what counts, once they are there.  scale_a(s, row): the row's word of four bytes (E2M1) or its byte
 // (E4M3), scale_b(s, row): its byte.  Returns whether some scale that this
 // thread loaded was outside the window.
-template <bool A8, int WM, typename LA, typename LB, typename CUT, typename SA, typename SB>
+template <bool A8, int WM, typename LA, typename LB, typename CA, typename CB, typename SA,
+          typename SB>
 __device__ __forceinline__ bool bf16_tile(Bf16Shared<A8, WM>& sh, int stages, int full_stages,
-                                          LA load_a, LB load_b, CUT cut, SA scale_a, SB scale_b,
+                                          LA load_a, LB load_b, CA cut_a, CB cut_b, SA scale_a, SB scale_b,
                                           f32x16 (&acc)[4][2]) {
   constexpr int T = 128 * WM, kBM = 64 * WM;
   constexpr int kPerA = Bf16Shared<A8, WM>::kA / 16, kLA = kBN * kPerA / T, kLB = kBM * 8 / T;
@@ -374,11 +376,11 @@ __device__ __forceinline__ bool bf16_tile(Bf16Shared<A8, WM>& sh, int stages, in
   const int wn = wave & 1, wm = wave >> 1, r = lane & 31, g = lane >> 5;
   i32x4 ra[kLA], rb[kLB];
   bool odd_scale = false;
-  auto fetch = [&](int s) {
+  auto fetch = [&](auto first, int s) {
 #pragma unroll
-    for (int i = 0; i < kLA; ++i) ra[i] = load_a(s, i);
+    for (int i = 0; i < kLA; ++i) ra[i] = load_a(first, s, i);
 #pragma unroll
-    for (int i = 0; i < kLB; ++i) rb[i] = load_b(s, i);
+    for (int i = 0; i < kLB; ++i) rb[i] = load_b(first, s, i);
   };
   // T / C is a multiple of 8, so a thread's rows share their place in the pattern
   const int put8 = (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4);
@@ -387,9 +389,9 @@ __device__ __forceinline__ bool bf16_tile(Bf16Shared<A8, WM>& sh, int stages, in
     const int b = s & 1;
     if (s >= full_stages) {
 #pragma unroll
-      for (int i = 0; i < kLA; ++i) cut(s, tid % kPerA, ra[i]);
+      for (int i = 0; i < kLA; ++i) cut_a(s, i, ra[i]);
 #pragma unroll
-      for (int i = 0; i < kLB; ++i) cut(s, tid % 8, rb[i]);
+      for (int i = 0; i < kLB; ++i) cut_b(s, i, rb[i]);
     }
 #pragma unroll
     for (int i = 0; i < kLA; ++i)
@@ -457,12 +459,12 @@ __device__ __forceinline__ bool bf16_tile(Bf16Shared<A8, WM>& sh, int stages, in
     }
   };
   if (stages == 0) return false;
-  fetch(0);
+  fetch(std::true_type(), 0);
   put_scales(0);
   put(0);
   __syncthreads();
   for (int s = 0; s < stages; ++s) {
-    fetch(min(s + 1, stages - 1));
+    fetch(std::false_type(), min(s + 1, stages - 1));
     compute(s);
     // the products stay before what follows: sums left for later would be
     // moved past the branches to the end of the loop

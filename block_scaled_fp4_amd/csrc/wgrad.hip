@@ -20,20 +20,30 @@ struct WgradArgs {
 };
 
 // 16 tokens from t of a channel of `count`, at any byte alignment.  Tokens past
-// the end are not read: the load ends at the last token, and cut_tokens16
-// shifts it down, so that they count as zero.
+// the end count as zero: the load ends at the last token and is shifted down
+// (drop_bytes), or, of a shard of fewer than 16, runs into the next channels and
+// is masked (keep_bytes).
 __device__ __forceinline__ i32x4 load_tokens16(const uint8_t* ch, uint32_t t) {
   i32x4 v;
   memcpy(&v, ch + t, 16);
   return v;
 }
-__device__ __forceinline__ void cut_tokens16(int t, int count, i32x4& v) {   // count >= 16
-  const int drop = min(t - min(t, count - 16), 16) * 8, d = drop & 63;
+// v without its lowest `drop` bytes, 0 <= drop <= 16.
+__device__ __forceinline__ void drop_bytes(int drop, i32x4& v) {
   uint64_t q[2];
   memcpy(q, &v, 16);
+  const int d = (drop * 8) & 63;
   const uint64_t hi = q[1] >> d, lo = d ? (q[0] >> d) | (q[1] << (64 - d)) : q[0];
-  const uint64_t l = drop < 64 ? lo : (drop < 128 ? hi : 0), h = drop < 64 ? hi : 0;
+  const uint64_t l = drop < 8 ? lo : (drop < 16 ? hi : 0), h = drop < 8 ? hi : 0;
   v = i32x4{(int)l, (int)(l >> 32), (int)h, (int)(h >> 32)};
+}
+// Only the lowest `keep` bytes of v, keep <= 16 (none where it is negative).
+__device__ __forceinline__ void keep_bytes(int keep, i32x4& v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = keep - 4 * i;
+    v[i] = k <= 0 ? 0 : (k >= 4 ? v[i] : (int)((uint32_t)v[i] & ((1u << (8 * k)) - 1u)));
+  }
 }
 // The same for any count, byte by byte.
 __device__ __forceinline__ i32x4 load_few_tokens16(const uint8_t* ch, int t, int count) {
@@ -128,26 +138,44 @@ __global__ __launch_bounds__(128 * WM, 1) void wgrad_tiles_kernel(WgradArgs p, i
   const int64_t orow = (int64_t)e * p.m;
   const TileView view = {a, b, as, bs, cnt, blocks, mrows, nrows};
   f32x16 acc[4][2] = {};
-  // rare cases go 16 x 16 at a time, straight from memory: scales outside the
-  // bf16 window over codes, and shards too short for a load of 16 tokens
-  bool rare = cnt > 0 && cnt < 16;
   // a thread's rows are 16 WM apart; with only 128 rows left on a side, those
   // past them are the first again
   const int ch = (threadIdx.x & 7) * 16;
   const uint32_t row_at = (threadIdx.x >> 3) * (uint32_t)cnt;
   const int64_t step = (int64_t)(16 * WM) * cnt;
   const int ia = nrows >= kBN ? 15 : 128 / (16 * WM) - 1, ib = mrows >= kBM ? 15 : 128 / (16 * WM) - 1;
-  if (!rare) {
-    const bool odd = bf16_tile<true, WM>(
-        sh.t, blocks, cnt >> 7,
-        [&](int s, int i) { return load_tokens16(b + (i & ia) * step, row_at + (uint32_t)min(s * 128 + ch, cnt - 16)); },
-        [&](int s, int i) { return load_tokens16(a + (i & ib) * step, row_at + (uint32_t)min(s * 128 + ch, cnt - 16)); },
-        [&](int s, int c, i32x4& v) { cut_tokens16(s * 128 + c * 16, cnt, v); },
-        [&](int s, int row) { return e8m0_of(bs[(int64_t)min(row, nrows - 1) * blocks + s]); },
-        [&](int s, int row) { return e8m0_of(as[(int64_t)min(row, mrows - 1) * blocks + s]); }, acc);
-    rare = __syncthreads_or(odd) && __syncthreads_or(scales_need_care<kBM>(view));
-  }
-  if (rare) {
+  // With fewer than 16 tokens a load runs into the next channels, and at the end
+  // of the operand begins `over` bytes early.
+  const int64_t a_end = (int64_t)p.m * p.tokens - (a - p.a), b_end = (int64_t)p.n * p.tokens - (b - p.b);
+  auto over = [&](int64_t end, int64_t row0) { return (int)max(row0 + row_at + 16 - end, (int64_t)0); };
+  const bool few = cnt < 16;
+  // They are one stage, so that what the loop loads ahead only has to be there.
+  const uint32_t row_in = few ? 0 : row_at;
+  const int last = max(cnt - 16, 0), ia_in = few ? 0 : ia, ib_in = few ? 0 : ib;
+  auto load = [&](auto first, const uint8_t* ch0, int64_t end, int i, int mask, int mask_in, int s) {
+    if constexpr (decltype(first)::value) {
+      if (few) return load_tokens16(ch0 + (i & mask) * step - over(end, (i & mask) * step), row_at);
+    }
+    return load_tokens16(ch0 + (i & mask_in) * step, row_in + (uint32_t)min(s * 128 + ch, last));
+  };
+  auto cut = [&](int64_t end, int64_t row0, int s, i32x4& v) {
+    const int t = s * 128 + ch;
+    if (few) {
+      drop_bytes(over(end, row0), v);
+      keep_bytes(cnt - t, v);
+    } else {
+      drop_bytes(min(t - min(t, cnt - 16), 16), v);
+    }
+  };
+  const bool odd = bf16_tile<true, WM>(
+      sh.t, blocks, cnt >> 7,
+      [&](auto first, int s, int i) { return load(first, b, b_end, i, ia, ia_in, s); },
+      [&](auto first, int s, int i) { return load(first, a, a_end, i, ib, ib_in, s); },
+      [&](int s, int i, i32x4& v) { cut(b_end, (i & ia) * step, s, v); },
+      [&](int s, int i, i32x4& v) { cut(a_end, (i & ib) * step, s, v); },
+      [&](int s, int row) { return e8m0_of(bs[(int64_t)min(row, nrows - 1) * blocks + s]); },
+      [&](int s, int row) { return e8m0_of(as[(int64_t)min(row, mrows - 1) * blocks + s]); }, acc);
+  if (__syncthreads_or(odd) && __syncthreads_or(scales_need_care<kBM>(view))) {
     rare_quarter<BF16>(view, mw - m0, nw - n0, p.out, orow + m0, p.n, n0);
     return;
   }

@@ -129,3 +129,12 @@ def test_larger_outputs(counts, M, N):
     the end of either side."""
     m = need_gpu()
     check(m, np.random.default_rng(M), counts, M - 128, N, "f32" if M < 2000 else "bf16")
+
+
+@pytest.mark.parametrize("last", list(range(1, 18)))
+def test_few_tokens_at_the_end(last):
+    """Shards of 1 to 17 tokens in the middle and at the end of the operands:
+    every byte alignment, and loads that would pass the end."""
+    m = need_gpu()
+    check(m, np.random.default_rng(last), [3, last, 0, 20 - last, 1, last], 128, 384, "f32")
+    check(m, np.random.default_rng(last), [last], 256, 128, "f32")

@@ -326,41 +326,55 @@ def mxfp4_row_to_fp8_row(packed, scales_e8m0, hidden, fp8_out=None, fp8_scales=N
     return fp8_out, fp8_scales
 
 
-def _rows_fmt(scales):
-    """The row format that goes with block scales of this dtype."""
-    return "fp8" if scales.dtype == torch.float32 else "mxfp4"
+def _fits(t, dtype, numel, gpu):
+    """_arg's conditions for a tensor on GPU number `gpu`, without its messages."""
+    return t.dtype is dtype and t.get_device() == gpu and t.is_contiguous() and t.numel() >= numel
 
 
-def _row_operand(name, t, scales, rows, device):
-    """Checks one quantized operand of `rows` rows; returns its K."""
-    if t.dtype == torch.float8_e4m3fn:
-        t = t.view(torch.uint8)
-    fp8 = _rows_fmt(scales) == "fp8"
-    cols = t.shape[-1] if fp8 else 2 * t.shape[-1]
-    _arg(t, name, torch.uint8, rows * (cols if fp8 else cols // 2), device)
-    _arg(scales, name + "_scales", torch.float32 if fp8 else torch.uint8,
-         rows * (cols // 128 if fp8 else cols // 32), device)
-    return cols
+def _codes(t):
+    """E4M3 codes as bytes, whichever dtype they came in."""
+    return t.view(torch.uint8) if t.dtype is torch.float8_e4m3fn else t
 
 
-def _product_args(a, a_scales, a_row_scale, w, w_scales, out_dtype, out):
-    """Checks what both products share; returns (M, N, K, out)."""
-    _dev(a)
-    _dev(w)
-    if w_scales.dtype != torch.uint8:
-        raise TypeError(f"weight scales must be torch.uint8, got {w_scales.dtype}")
-    M, N = a.numel() // a.shape[-1] if a.shape[-1] else 0, w.shape[-2]
-    K = _row_operand("a", a, a_scales, M, a.device)
-    Kw = _row_operand("w", w, w_scales, w.numel() // w.shape[-1] if w.shape[-1] else 0, a.device)
-    if K != Kw:
-        raise ValueError(f"a has {K} columns, the weights have {Kw}")
-    if a_row_scale is not None:
-        _arg(a_row_scale, "a_row_scale", torch.float32, M, a.device)
+def _product(name, a, a_scales, a_row_scale, w, w_scales, offsets, out_dtype, out, stream):
+    """Checks and launches either product (small sizes are over in the time
+    that a call takes here, so the common case is one run of plain tests)."""
+    a = _codes(a)
+    shape, gpu = a.shape, a.get_device()
+    fp8 = a_scales.dtype is torch.float32
+    width, N, kb = shape[-1], w.shape[-2], w.shape[-1]
+    M = a.numel() // width if width else 0
+    K = 2 * kb
+    E = 1 if offsets is None else w.shape[0]
+    if (width if fp8 else 2 * width) != K:
+        raise ValueError(f"a has {width if fp8 else 2 * width} columns, the weights have {K}")
     if out is None:
-        out = torch.empty((*a.shape[:-1], N), dtype=out_dtype, device=a.device)
-    else:
+        out = torch.empty((M, N) if len(shape) == 2 else (*shape[:-1], N), dtype=out_dtype, device=a.device)
+    sdt, sn = (torch.float32, M * (K // 128)) if fp8 else (torch.uint8, M * (K // 32))
+    if not (gpu >= 0 and _fits(a, torch.uint8, M * width, gpu) and _fits(a_scales, sdt, sn, gpu)
+            and _fits(w, torch.uint8, E * N * kb, gpu) and _fits(w_scales, torch.uint8, E * N * (K // 32), gpu)
+            and _fits(out, out.dtype, M * N, gpu)
+            and (a_row_scale is None or _fits(a_row_scale, torch.float32, M, gpu))
+            and (offsets is None or _fits(offsets, torch.int64, E + 1, gpu))):
+        _dev(a)
+        _arg(a, "a", torch.uint8, M * width, a.device)
+        _arg(a_scales, "a_scales", sdt, sn, a.device)
+        _arg(w, "w", torch.uint8, E * N * kb, a.device)
+        _arg(w_scales, "w_scales", torch.uint8, E * N * (K // 32), a.device)
         _arg(out, "out", out.dtype, M * N, a.device)
-    return M, N, K, out
+        _arg(a_row_scale, "a_row_scale", torch.float32, M, a.device, optional=True)
+        _arg(offsets, "token_offsets", torch.int64, E + 1, a.device, optional=True)
+    row = None if a_row_scale is None else a_row_scale.data_ptr()
+    if offsets is None:
+        status = _lib.mxfp4_matmul(a.data_ptr(), fp8, a_scales.data_ptr(), row, w.data_ptr(),
+                                   w_scales.data_ptr(), M, N, K, out.data_ptr(),
+                                   _dtype_code(out.dtype), _stream(stream))
+    else:
+        status = _lib.mxfp4_matmul_grouped(a.data_ptr(), fp8, a_scales.data_ptr(), row, w.data_ptr(),
+                                           w_scales.data_ptr(), offsets.data_ptr(), E, M, N, K,
+                                           out.data_ptr(), _dtype_code(out.dtype), _stream(stream))
+    _check(name, status)
+    return out
 
 
 def mxfp4_matmul(a, a_scales, b, b_scales, a_row_scale=None, out_dtype=torch.bfloat16, out=None,
@@ -373,11 +387,7 @@ def mxfp4_matmul(a, a_scales, b, b_scales, a_row_scale=None, out_dtype=torch.bfl
     per row of a, such as rmsnorm_quantize's row_scale."""
     if b.dim() != 2:
         raise ValueError("b must be [N, K/2]")
-    M, N, K, out = _product_args(a, a_scales, a_row_scale, b, b_scales, out_dtype, out)
-    _check("mxfp4_matmul", _lib.mxfp4_matmul(
-        _ptr(a), ROWS[_rows_fmt(a_scales)], _ptr(a_scales), _ptr(a_row_scale), _ptr(b),
-        _ptr(b_scales), M, N, K, _ptr(out), _dtype_code(out.dtype), _stream(stream)))
-    return out
+    return _product("mxfp4_matmul", a, a_scales, a_row_scale, b, b_scales, None, out_dtype, out, stream)
 
 
 def mxfp4_matmul_grouped(a, a_scales, w, w_scales, token_offsets, a_row_scale=None,
@@ -386,14 +396,10 @@ def mxfp4_matmul_grouped(a, a_scales, w, w_scales, token_offsets, a_row_scale=No
     w MXFP4 [E, N, K/2] -> [T, N].  Operands as mxfp4_matmul."""
     if w.dim() != 3:
         raise ValueError("w must be [E, N, K/2]")
-    M, N, K, out = _product_args(a, a_scales, a_row_scale, w, w_scales, out_dtype, out)
-    E = w.shape[0]
-    _arg(token_offsets, "token_offsets", torch.int64, E + 1, a.device)
-    _check("mxfp4_matmul_grouped", _lib.mxfp4_matmul_grouped(
-        _ptr(a), ROWS[_rows_fmt(a_scales)], _ptr(a_scales), _ptr(a_row_scale), _ptr(w),
-        _ptr(w_scales), _ptr(token_offsets), E, M, N, K, _ptr(out), _dtype_code(out.dtype),
-        _stream(stream)))
-    return out
+    if token_offsets is None:
+        raise ValueError("token_offsets is required")
+    return _product("mxfp4_matmul_grouped", a, a_scales, a_row_scale, w, w_scales, token_offsets,
+                    out_dtype, out, stream)
 
 
 def fp8_matmul_tokblk(a, a_scales, b, b_scales, token_offsets, m, n, out_dtype=torch.bfloat16,
@@ -402,22 +408,25 @@ def fp8_matmul_tokblk(a, a_scales, b, b_scales, token_offsets, m, n, out_dtype=t
 
     Operands as mxfp4_row_to_fp8_col_tokblk returns them (flat E4M3 columns and
     flat fp32 scales) for hidden sizes m and n and the same token_offsets."""
-    _dev(a)
-    T = a.numel() // m if m else 0
-    E = token_offsets.numel() - 1
-    for t, s, h, name in ((a, a_scales, m, "a"), (b, b_scales, n, "b")):
-        if t.dtype == torch.float8_e4m3fn:
-            t = t.view(torch.uint8)
-        _arg(t, name, torch.uint8, T * h, a.device)
-        _arg(s, name + "_scales", torch.float32, tokblk_scale_count(T, E, h), a.device)
-    _arg(token_offsets, "token_offsets", torch.int64, 1, a.device)
+    a, b = _codes(a), _codes(b)
+    gpu, T, E = a.get_device(), a.numel() // m if m else 0, token_offsets.numel() - 1
+    na, nb = tokblk_scale_count(T, E, m), tokblk_scale_count(T, E, n)
     if out is None:
         out = torch.empty((E, m, n), dtype=out_dtype, device=a.device)
-    else:
+    if not (gpu >= 0 and _fits(a, torch.uint8, T * m, gpu) and _fits(b, torch.uint8, T * n, gpu)
+            and _fits(a_scales, torch.float32, na, gpu) and _fits(b_scales, torch.float32, nb, gpu)
+            and _fits(token_offsets, torch.int64, 1, gpu) and _fits(out, out.dtype, E * m * n, gpu)):
+        _dev(a)
+        _arg(a, "a", torch.uint8, T * m, a.device)
+        _arg(b, "b", torch.uint8, T * n, a.device)
+        _arg(a_scales, "a_scales", torch.float32, na, a.device)
+        _arg(b_scales, "b_scales", torch.float32, nb, a.device)
+        _arg(token_offsets, "token_offsets", torch.int64, 1, a.device)
         _arg(out, "out", out.dtype, E * m * n, a.device)
     _check("fp8_matmul_tokblk", _lib.fp8_matmul_tokblk(
-        _ptr(a), _ptr(a_scales), _ptr(b), _ptr(b_scales), _ptr(token_offsets), E, T, m, n,
-        _ptr(out), _dtype_code(out.dtype), _stream(stream)))
+        a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(),
+        token_offsets.data_ptr(), E, T, m, n, out.data_ptr(), _dtype_code(out.dtype),
+        _stream(stream)))
     return out
 
 
@@ -430,29 +439,36 @@ def rmsnorm_quantize(x, weight, residual=None, eps=1e-6, fmt="fp8", q=None, scal
     q E4M3 uint8 [.., cols], scales fp32 [.., cols/128].  The rows hold
     h * weight; row_scale (fp32, one per row) is 1 / rms, the a_row_scale of
     the products.  Without a residual, and without an h to fill, h is x."""
-    _dev(x)
-    cols = x.shape[-1]
+    shape, gpu, dt = x.shape, x.get_device(), x.dtype
+    cols = shape[-1]
     rows = x.numel() // cols if cols else 0
-    lead = x.shape[:-1]
-    per, block, sdt = (1, 128, torch.float32) if fmt == "fp8" else (2, 32, torch.uint8)
+    lead, fp8 = shape[:-1], fmt == "fp8"
+    per, block, sdt = (1, 128, torch.float32) if fp8 else (2, 32, torch.uint8)
     if q is None:
-        q = torch.empty((*lead, cols // per), dtype=torch.uint8, device=x.device)
+        q = (torch.empty_like(x, dtype=torch.uint8) if fp8 else
+             torch.empty((*lead, cols // 2), dtype=torch.uint8, device=x.device))
     if scales is None:
         scales = torch.empty((*lead, cols // block), dtype=sdt, device=x.device)
     if row_scale is None:
         row_scale = torch.empty(lead, dtype=torch.float32, device=x.device)
     if h is None and residual is not None:
         h = torch.empty_like(x)
-    _arg(q, "q", torch.uint8, rows * cols // per, x.device)
-    _arg(scales, "scales", sdt, rows * (cols // block), x.device)
-    _arg(row_scale, "row_scale", torch.float32, rows, x.device)
-    _arg(residual, "residual", x.dtype, rows * cols, x.device, optional=True)
-    _arg(h, "h", x.dtype, rows * cols, x.device, optional=True)
-    _arg(weight, "weight", weight.dtype, cols, x.device)
+    n = rows * cols
+    if not (gpu >= 0 and _fits(x, dt, n, gpu) and _fits(q, torch.uint8, n // per, gpu)
+            and _fits(scales, sdt, rows * (cols // block), gpu) and _fits(row_scale, torch.float32, rows, gpu)
+            and (residual is None or _fits(residual, dt, n, gpu)) and (h is None or _fits(h, dt, n, gpu))
+            and _fits(weight, weight.dtype, cols, gpu)):
+        _dev(x)
+        _arg(q, "q", torch.uint8, n // per, x.device)
+        _arg(scales, "scales", sdt, rows * (cols // block), x.device)
+        _arg(row_scale, "row_scale", torch.float32, rows, x.device)
+        _arg(residual, "residual", dt, n, x.device, optional=True)
+        _arg(h, "h", dt, n, x.device, optional=True)
+        _arg(weight, "weight", weight.dtype, cols, x.device)
     _check("rmsnorm_quantize", _lib.rmsnorm_quantize(
-        _ptr(x), _ptr(residual), _dtype_code(x.dtype), _ptr(weight), _dtype_code(weight.dtype),
-        rows, cols, eps, ROWS.get(fmt, 99), _ptr(q), _ptr(scales), _ptr(row_scale), _ptr(h),
-        _stream(stream)))
+        x.data_ptr(), _ptr(residual), _dtype_code(dt), weight.data_ptr(), _dtype_code(weight.dtype),
+        rows, cols, eps, ROWS.get(fmt, 99), q.data_ptr(), scales.data_ptr(), row_scale.data_ptr(),
+        _ptr(h), _stream(stream)))
     return q, scales, row_scale, x if h is None else h
 
 
@@ -461,27 +477,31 @@ def rmsnorm_backward(dy, h, weight, row_scale, dh=None, dx=None, dweight=None, w
     """Gradient of row_scale * h * weight -> (dx, dweight fp32 [cols]); dh, if
     given, is added to dx.  workspace: uint8 of at least
     rmsnorm_backward_workspace(rows, cols) elements (allocated if None)."""
-    _dev(dy)
-    cols = dy.shape[-1]
+    gpu, dt, cols = dy.get_device(), dy.dtype, dy.shape[-1]
     rows = dy.numel() // cols if cols else 0
-    need = rmsnorm_backward_workspace(rows, cols)
+    n, need = rows * cols, _lib.rmsnorm_backward_workspace(rows, cols)
     if dx is None:
         dx = torch.empty_like(dy)
     if dweight is None:
         dweight = torch.empty(cols, dtype=torch.float32, device=dy.device)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dy.device)
-    _arg(h, "h", dy.dtype, rows * cols, dy.device)
-    _arg(dh, "dh", dy.dtype, rows * cols, dy.device, optional=True)
-    _arg(dx, "dx", dy.dtype, rows * cols, dy.device)
-    _arg(weight, "weight", weight.dtype, cols, dy.device)
-    _arg(row_scale, "row_scale", torch.float32, rows, dy.device)
-    _arg(dweight, "dweight", torch.float32, cols, dy.device)
-    _arg(workspace, "workspace", torch.uint8, need, dy.device)
+    if not (gpu >= 0 and _fits(dy, dt, n, gpu) and _fits(h, dt, n, gpu) and _fits(dx, dt, n, gpu)
+            and (dh is None or _fits(dh, dt, n, gpu)) and _fits(weight, weight.dtype, cols, gpu)
+            and _fits(row_scale, torch.float32, rows, gpu) and _fits(dweight, torch.float32, cols, gpu)
+            and _fits(workspace, torch.uint8, need, gpu)):
+        _dev(dy)
+        _arg(h, "h", dt, n, dy.device)
+        _arg(dh, "dh", dt, n, dy.device, optional=True)
+        _arg(dx, "dx", dt, n, dy.device)
+        _arg(weight, "weight", weight.dtype, cols, dy.device)
+        _arg(row_scale, "row_scale", torch.float32, rows, dy.device)
+        _arg(dweight, "dweight", torch.float32, cols, dy.device)
+        _arg(workspace, "workspace", torch.uint8, need, dy.device)
     _check("rmsnorm_backward", _lib.rmsnorm_backward(
-        _ptr(dy), _ptr(h), _ptr(dh), _dtype_code(dy.dtype), _ptr(weight),
-        _dtype_code(weight.dtype), _ptr(row_scale), rows, cols, _ptr(dx), _ptr(dweight),
-        _ptr(workspace), workspace.numel(), _stream(stream)))
+        dy.data_ptr(), h.data_ptr(), _ptr(dh), _dtype_code(dt), weight.data_ptr(),
+        _dtype_code(weight.dtype), row_scale.data_ptr(), rows, cols, dx.data_ptr(),
+        dweight.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)))
     return dx, dweight
 
 

@@ -376,11 +376,13 @@ __device__ __forceinline__ bool bf16_tile(Bf16Shared<A8, WM>& sh, int stages, in
   const int wn = wave & 1, wm = wave >> 1, r = lane & 31, g = lane >> 5;
   i32x4 ra[kLA], rb[kLB];
   bool odd_scale = false;
-  auto fetch = [&](auto first, int s) {
+  auto fetch_some = [&](auto first, int s, int from, int to) {
 #pragma unroll
-    for (int i = 0; i < kLA; ++i) ra[i] = load_a(first, s, i);
-#pragma unroll
-    for (int i = 0; i < kLB; ++i) rb[i] = load_b(first, s, i);
+    for (int i = 0; i < kLA + kLB; ++i) {
+      if (i < from || i >= to) continue;
+      if (i < kLA) ra[i < kLA ? i : 0] = load_a(first, s, i);
+      else rb[i < kLA ? 0 : i - kLA] = load_b(first, s, i - kLA);
+    }
   };
   // T / C is a multiple of 8, so a thread's rows share their place in the pattern
   const int put8 = (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4);
@@ -423,7 +425,7 @@ __device__ __forceinline__ bool bf16_tile(Bf16Shared<A8, WM>& sh, int stages, in
     }
   };
   const int rb0 = (wm * 64 + r) * 128, ra0 = (wn * 128 + r) * Bf16Shared<A8, WM>::kA;
-  auto compute = [&](int s) {
+  auto compute = [&](int s, auto before) {   // before(i), i = 0 .. 7: ahead of the i-th eighth
     const int b = s & 1, sj = s & 7;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
@@ -439,6 +441,7 @@ __device__ __forceinline__ bool bf16_tile(Bf16Shared<A8, WM>& sh, int stages, in
       }
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
+        before(ks * 4 + f);
         Frag<A8> v;
         float sc;
         if constexpr (A8) {
@@ -459,13 +462,18 @@ __device__ __forceinline__ bool bf16_tile(Bf16Shared<A8, WM>& sh, int stages, in
     }
   };
   if (stages == 0) return false;
-  fetch(std::true_type(), 0);
+  fetch_some(std::true_type(), 0, 0, kLA + kLB);
   put_scales(0);
   put(0);
   __syncthreads();
   for (int s = 0; s < stages; ++s) {
-    fetch(std::false_type(), min(s + 1, stages - 1));
-    compute(s);
+    // the next stage's loads go out an eighth at a time: issued together they
+    // would hold the products up until the last is taken
+    const int next = min(s + 1, stages - 1);
+    compute(s, [&](int i) {
+      __builtin_amdgcn_sched_barrier(0);
+      fetch_some(std::false_type(), next, i * (kLA + kLB) / 8, (i + 1) * (kLA + kLB) / 8);
+    });
     // the products stay before what follows: sums left for later would be
     // moved past the branches to the end of the loop
 #pragma unroll

@@ -260,14 +260,16 @@ __device__ __forceinline__ void store_out4(void* out, int64_t row, int n_cols, i
 }
 
 // 16 bytes at `src`: eight bf16 or four fp32 consecutive columns from n of one
-// output row; columns past the row's end are dropped.
+// output row; columns past the row's end are dropped.  Nontemporal: outputs of
+// whole tiles would push the operands out of the caches (the gradient of 16 x
+// 4096 x 7168: 1167 -> 1033 us, 8192^3 in MXFP4: 267 -> 256 us).
 template <bool BF16>
 __device__ __forceinline__ void store_chunk(void* out, int64_t row, int n_cols, int n,
                                             const uint8_t* src) {
   constexpr int kEl = BF16 ? 8 : 4;
   uint8_t* dst = static_cast<uint8_t*>(out) + (row * n_cols + n) * (16 / kEl);
   if (n + kEl <= n_cols && n_cols % kEl == 0) {
-    *reinterpret_cast<u32x4*>(dst) = *reinterpret_cast<const u32x4*>(src);
+    st_u32x4(dst, *reinterpret_cast<const u32x4*>(src));
   } else {
 #pragma unroll 1
     for (int j = 0; j < min(kEl, n_cols - n); ++j) {

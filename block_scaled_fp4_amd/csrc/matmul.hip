@@ -23,26 +23,19 @@ struct LaneStep {   // one lane's part of one 16-row operand at one step
   int s;
 };
 
-// Row `row` of an operand at step `st`, group g.  KT: the last step may be
-// short, and what lies past K counts as zero (and is not read).
-template <bool A8, bool KT>
+// Row `row` of an operand at step `st`, group g.
+template <bool A8>
 __device__ __forceinline__ void load_lane(const uint8_t* base, const void* scales, int64_t row,
                                           int k, int st, int g, LaneStep<A8>& o) {
-  const int kk = st * 128 + 32 * g;
-  const bool in = !KT || kk < k;
-  const int at = in ? kk : 0;
+  const int at = st * 128 + 32 * g;
   if constexpr (A8) {
     const i32x4* p = reinterpret_cast<const i32x4*>(base + row * k + at);
     o.v.lo = p[0];
     o.v.hi = p[1];
-    o.s = (int)e8m0_of(static_cast<const float*>(scales)[row * (k >> 7) + (at >> 7)]);
+    o.s = (int)e8m0_of(static_cast<const float*>(scales)[row * (k >> 7) + st]);
   } else {
     o.v.lo = *reinterpret_cast<const i32x4*>(base + row * (k >> 1) + (at >> 1));
     o.s = static_cast<const uint8_t*>(scales)[row * (k >> 5) + (at >> 5)];
-    if (KT && !in) {
-      o.v.lo = i32x4{0, 0, 0, 0};
-      o.s = 127;
-    }
   }
 }
 
@@ -81,7 +74,7 @@ __global__ __launch_bounds__(64 * W) void product_rows_kernel(ProductArgs p, int
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t blk = (int64_t)blockIdx.x + blk0;
   const int nt = (int)(blk % p.n_tiles), mt = (int)(blk / p.n_tiles);
-  int e = 0, row0 = mt * (16 * FM), row_end = (int)p.tokens;
+  int e = 0, row0 = p.offsets ? 0 : mt * (16 * FM), row_end = (int)p.tokens;
   if (p.offsets) {
     if (!locate_tile<16 * FM>(p.offsets, p.experts, (int)p.tokens, mt, e, row0, row_end)) return;
   }
@@ -100,6 +93,11 @@ __global__ __launch_bounds__(64 * W) void product_rows_kernel(ProductArgs p, int
     LaneStep<false> w[U][FN];
     LaneStep<A8> a[U][FM];
   } even = {}, odd = {};   // in turn, so that no load is waited for before its use
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+      if (A8) even.a[u][f].s = odd.a[u][f].s = 127;   // of lanes without a token: inside the window
   // Loads are counted here, not bytes: one instruction takes the scales of U
   // steps, and with few tokens lanes past the last load nothing.
   const int kb = p.k >> 1, ksb = p.k >> 5;
@@ -254,7 +252,7 @@ __global__ __launch_bounds__(256, 1) void product_tiles_kernel(ProductArgs p, in
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t blk = (int64_t)blockIdx.x + blk0;
   const int nt = (int)(blk % p.n_tiles), mt = (int)(blk / p.n_tiles);
-  int e = 0, row0 = mt * BM, row_end = (int)p.tokens;
+  int e = 0, row0 = p.offsets ? 0 : mt * BM, row_end = (int)p.tokens;
   if (p.offsets) {
     if (!locate_tile<BM>(p.offsets, p.experts, (int)p.tokens, mt, e, row0, row_end)) return;
   }
@@ -470,8 +468,8 @@ __device__ __attribute__((noinline)) bool scales_need_care(Fp8TileView v) {
   for (int i = 0; i < v.k >> 5; ++i) {
     LaneStep<false> lw;
     LaneStep<true> lx;
-    load_lane<false, false>(v.w, v.ws, min((int)threadIdx.x % kBN, v.wrows - 1), v.k, i >> 2, i & 3, lw);
-    load_lane<true, false>(v.x, v.xs, min((int)threadIdx.x % 128, v.xrows - 1), v.k, i >> 2, i & 3, lx);
+    load_lane<false>(v.w, v.ws, min((int)threadIdx.x % kBN, v.wrows - 1), v.k, i >> 2, i & 3, lw);
+    load_lane<true>(v.x, v.xs, min((int)threadIdx.x % 128, v.xrows - 1), v.k, i >> 2, i & 3, lx);
     bad |= !scale_fits(lw) || !scale_fits(lx);
   }
   return bad;
@@ -492,8 +490,8 @@ __device__ __attribute__((noinline)) void rare_quarter(Fp8TileView v, int mw, in
     f32x4 c[1][1] = {};
 #pragma unroll 1
     for (int s = 0; s < v.k >> 7; ++s) {
-      load_lane<false, false>(v.w, v.ws, min(n + r, v.wrows - 1), v.k, s, g, lw[0]);
-      load_lane<true, false>(v.x, v.xs, min(m + r, v.xrows - 1), v.k, s, g, lx[0]);
+      load_lane<false>(v.w, v.ws, min(n + r, v.wrows - 1), v.k, s, g, lw[0]);
+      load_lane<true>(v.x, v.xs, min(m + r, v.xrows - 1), v.k, s, g, lx[0]);
       mfma_bf16_step(lw, lx, c);
     }
     if (m + r < v.xrows) {
@@ -515,7 +513,7 @@ __global__ __launch_bounds__(256, 2) void product_fp8_tiles_kernel(ProductArgs p
   } sh;
   const int64_t blk = (int64_t)blockIdx.x + blk0;
   const int nt = (int)(blk % p.n_tiles), mt = (int)(blk / p.n_tiles);
-  int e = 0, row0 = mt * kBM, row_end = (int)p.tokens;
+  int e = 0, row0 = p.offsets ? 0 : mt * kBM, row_end = (int)p.tokens;
   if (p.offsets) {
     if (!locate_tile<kBM>(p.offsets, p.experts, (int)p.tokens, mt, e, row0, row_end)) return;
   }

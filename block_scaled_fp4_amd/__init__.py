@@ -349,7 +349,7 @@ def _product(name, a, a_scales, a_row_scale, w, w_scales, offsets, out_dtype, ou
     if (width if fp8 else 2 * width) != K:
         raise ValueError(f"a has {width if fp8 else 2 * width} columns, the weights have {K}")
     if out is None:
-        out = torch.empty((M, N) if len(shape) == 2 else (*shape[:-1], N), dtype=out_dtype, device=a.device)
+        out = a.new_empty((M, N) if len(shape) == 2 else (*shape[:-1], N), dtype=out_dtype)
     sdt, sn = (torch.float32, M * (K // 128)) if fp8 else (torch.uint8, M * (K // 32))
     if not (gpu >= 0 and _fits(a, torch.uint8, M * width, gpu) and _fits(a_scales, sdt, sn, gpu)
             and _fits(w, torch.uint8, E * N * kb, gpu) and _fits(w_scales, torch.uint8, E * N * (K // 32), gpu)
@@ -412,7 +412,7 @@ def fp8_matmul_tokblk(a, a_scales, b, b_scales, token_offsets, m, n, out_dtype=t
     gpu, T, E = a.get_device(), a.numel() // m if m else 0, token_offsets.numel() - 1
     na, nb = tokblk_scale_count(T, E, m), tokblk_scale_count(T, E, n)
     if out is None:
-        out = torch.empty((E, m, n), dtype=out_dtype, device=a.device)
+        out = a.new_empty((E, m, n), dtype=out_dtype)
     if not (gpu >= 0 and _fits(a, torch.uint8, T * m, gpu) and _fits(b, torch.uint8, T * n, gpu)
             and _fits(a_scales, torch.float32, na, gpu) and _fits(b_scales, torch.float32, nb, gpu)
             and _fits(token_offsets, torch.int64, 1, gpu) and _fits(out, out.dtype, E * m * n, gpu)):
@@ -446,11 +446,11 @@ def rmsnorm_quantize(x, weight, residual=None, eps=1e-6, fmt="fp8", q=None, scal
     per, block, sdt = (1, 128, torch.float32) if fp8 else (2, 32, torch.uint8)
     if q is None:
         q = (torch.empty_like(x, dtype=torch.uint8) if fp8 else
-             torch.empty((*lead, cols // 2), dtype=torch.uint8, device=x.device))
+             x.new_empty((*lead, cols // 2), dtype=torch.uint8))
     if scales is None:
-        scales = torch.empty((*lead, cols // block), dtype=sdt, device=x.device)
+        scales = x.new_empty((*lead, cols // block), dtype=sdt)
     if row_scale is None:
-        row_scale = torch.empty(lead, dtype=torch.float32, device=x.device)
+        row_scale = x.new_empty(lead, dtype=torch.float32)
     if h is None and residual is not None:
         h = torch.empty_like(x)
     n = rows * cols
@@ -483,9 +483,9 @@ def rmsnorm_backward(dy, h, weight, row_scale, dh=None, dx=None, dweight=None, w
     if dx is None:
         dx = torch.empty_like(dy)
     if dweight is None:
-        dweight = torch.empty(cols, dtype=torch.float32, device=dy.device)
+        dweight = dy.new_empty(cols, dtype=torch.float32)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dy.device)
+        workspace = dy.new_empty(need, dtype=torch.uint8)
     if not (gpu >= 0 and _fits(dy, dt, n, gpu) and _fits(h, dt, n, gpu) and _fits(dx, dt, n, gpu)
             and (dh is None or _fits(dh, dt, n, gpu)) and _fits(weight, weight.dtype, cols, gpu)
             and _fits(row_scale, torch.float32, rows, gpu) and _fits(dweight, torch.float32, cols, gpu)

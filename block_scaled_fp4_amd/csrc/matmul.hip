@@ -196,12 +196,14 @@ void launch_rows(ProductArgs p, int out_dtype, hipStream_t st) {
 // l: row l % 32, the 32 k of group l / 32; D's lane l: column l % 32, rows
 // 8 (i / 4) + 4 (l / 32) + i % 4).  A stage is 256 k: 128 bytes of every row go
 // to LDS with direct loads, two stages in turn, one barrier each.  A row's
-// eight 16-byte chunks lie at position chunk ^ (row % 8), so that neither the
-// line-wide direct loads nor the 32-row fragment reads meet a bank twice.
-// Bound by LDS (of a stage's 2048 matrix cycles, its fragment reads and writes
-// take over 1600) and, at each tile's start and end, by memory latency: 8192^3
-// in 253 us, 4.3 PFLOP/s; with the LDS reads, direct loads and scales left out,
-// the products alone take 183.
+// eight 16-byte chunks lie at position chunk ^ (row / 2 % 8), so that neither the
+// line-wide direct loads nor the 32-row fragment reads meet a bank twice (16
+// lanes of a read take all 64 banks: row parity picks the half, row / 2 the
+// place in it).
+// 8192^3 in 253 us, 4.3 PFLOP/s.  The matrix cores are busy 53% of the cycles,
+// at the 1.8 GHz that the card holds under this load; each of a compute unit's 4
+// tiles has 10 us of start and output around it, and with the LDS reads, direct
+// loads and scales left out the rest takes 183 us in place of 253.
 typedef __amdgpu_buffer_rsrc_t buffer_t;
 __device__ __forceinline__ buffer_t buffer_of(const void* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
@@ -263,8 +265,8 @@ __global__ __launch_bounds__(256, 1) void product_tiles_kernel(ProductArgs p, in
   const int stages = (p.k + 255) >> 8;
 
   // Direct loads: instruction i of this wave covers 8 rows; lane l is row
-  // l / 8, position l % 8, which holds chunk (l % 8) ^ (row % 8).
-  const int ch = (lane & 7) ^ (lane >> 3);
+  // l / 8, position l % 8, which holds chunk (l % 8) ^ (row / 2 % 8).
+  auto ch = [&](int i) { return (lane & 7) ^ (((i & 1) << 2) | (lane >> 4)); };
   const uint8_t* xa = p.a + (int64_t)row0 * kb;
   w += (int64_t)n0 * kb;
   ws += (int64_t)n0 * ksb;
@@ -272,10 +274,10 @@ __global__ __launch_bounds__(256, 1) void product_tiles_kernel(ProductArgs p, in
   uint32_t wo[2 * FN], xo[2 * FM];
 #pragma unroll
   for (int i = 0; i < 2 * FN; ++i)
-    wo[i] = (uint32_t)min(8 * (wave * 2 * FN + i) + (lane >> 3), wrows - 1) * (uint32_t)kb + ch * 16;
+    wo[i] = (uint32_t)min(8 * (wave * 2 * FN + i) + (lane >> 3), wrows - 1) * (uint32_t)kb + ch(i) * 16;
 #pragma unroll
   for (int i = 0; i < 2 * FM; ++i)
-    xo[i] = (uint32_t)min(8 * (wave * 2 * FM + i) + (lane >> 3), xrows - 1) * (uint32_t)kb + ch * 16;
+    xo[i] = (uint32_t)min(8 * (wave * 2 * FM + i) + (lane >> 3), xrows - 1) * (uint32_t)kb + ch(i) * 16;
   const buffer_t wb = buffer_of(w, (int64_t)min(wrows, BN) * kb);
   const buffer_t xb = buffer_of(xa, (int64_t)min(xrows, BM) * kb);
   // Stage s into buffer B.  In a last stage that reaches past K, the chunks
@@ -287,7 +289,7 @@ __global__ __launch_bounds__(256, 1) void product_tiles_kernel(ProductArgs p, in
     const int j = isw ? i : i - 2 * FN;
     uint32_t v = isw ? wo[j] : xo[j], so = s * 128;
     if (!decltype(full)::value && s * 256 + 256 > p.k) {
-      v += so - (uint32_t)max(s * 128 + ch * 16 + 16 - kb, 0);
+      v += so - (uint32_t)max(s * 128 + ch(j) * 16 + 16 - kb, 0);
       so = 0;
     }
     if (isw) load_to_lds(wb, v, so, &sh.t.w[B][(wave * 2 * FN + j) * 1024]);
@@ -336,7 +338,7 @@ __global__ __launch_bounds__(256, 1) void product_tiles_kernel(ProductArgs p, in
   const uint8_t *wl[4], *xl[4];   // this lane's chunk of its first fragment, for each 64 k
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
-    const int c = ((2 * ks + g) ^ (r & 7)) * 16;
+    const int c = ((2 * ks + g) ^ ((r >> 1) & 7)) * 16;
     wl[ks] = &sh.t.w[0][(wn * FN * 32 + r) * 128 + c];
     xl[ks] = &sh.t.x[0][(wm * FM * 32 + r) * 128 + c];
   }

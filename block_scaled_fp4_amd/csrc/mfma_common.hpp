@@ -344,8 +344,8 @@ __device__ __forceinline__ void store_quarter(const f32x16 (&acc)[FN][FM], uint8
 // each, and become bf16 values on their way to the instructions; each wave
 // converts 12 operand rows' worth for 64 instructions' time.
 //
-// E4M3 rows are 8 chunks of 16 bytes, chunk c at position c ^ (row % 8); E2M1
-// rows are 4 chunks, c at c ^ (row / 2 % 4): eight consecutive rows then touch
+// E4M3 rows are 8 chunks of 16 bytes, chunk c at position c ^ (row / 2 % 8); E2M1
+// rows are 4 chunks, c at c ^ (row / 4 % 4): 16 consecutive rows then touch
 // every bank once.  Scales lie beside for 8 stages at a time, one byte a row and
 // stage (E4M3, one block of 128) or four (E2M1): a stage's own few bytes of
 // each row would cost as many cache lines as its codes.
@@ -386,9 +386,9 @@ __device__ __forceinline__ bool bf16_tile(Bf16Shared<A8, WM>& sh, int stages, in
       else rb[i < kLA ? 0 : i - kLA] = load_b(first, s, i - kLA);
     }
   };
-  // T / C is a multiple of 8, so a thread's rows share their place in the pattern
-  const int put8 = (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4);
-  const int put4 = (tid >> 2) * 64 + (((tid & 3) ^ ((tid >> 3) & 3)) << 4);
+  // T / C is a multiple of 16, so a thread's rows share their place in the pattern
+  const int put8 = (tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 4) & 7)) << 4);
+  const int put4 = (tid >> 2) * 64 + (((tid & 3) ^ ((tid >> 4) & 3)) << 4);
   auto put = [&](int s) {
     const int b = s & 1;
     if (s >= full_stages) {
@@ -430,7 +430,7 @@ __device__ __forceinline__ bool bf16_tile(Bf16Shared<A8, WM>& sh, int stages, in
   // Fragment f of A, and both of B, for the ks-th 64 k of stage s, as codes.
   auto read_a = [&](int s, int ks, int f, Frag<A8>& v, float& sc) {
     const int b = s & 1, sj = s & 7;
-    const int c0 = ((4 * ks + 2 * g) ^ (r & 7)) << 4, c4 = ((2 * ks + g) ^ ((r >> 1) & 3)) << 4;
+    const int c0 = ((4 * ks + 2 * g) ^ ((r >> 1) & 7)) << 4, c4 = ((2 * ks + g) ^ ((r >> 2) & 3)) << 4;
     if constexpr (A8) {
       v.lo = *reinterpret_cast<const i32x4*>(&sh.a[b][ra0 + f * 32 * 128 + c0]);
       v.hi = *reinterpret_cast<const i32x4*>(&sh.a[b][ra0 + f * 32 * 128 + (c0 ^ 16)]);
@@ -441,7 +441,7 @@ __device__ __forceinline__ bool bf16_tile(Bf16Shared<A8, WM>& sh, int stages, in
     }
   };
   auto read_b = [&](int s, int ks, Frag<true> (&v)[2], float (&sc)[2]) {
-    const int b = s & 1, sj = s & 7, c0 = ((4 * ks + 2 * g) ^ (r & 7)) << 4;
+    const int b = s & 1, sj = s & 7, c0 = ((4 * ks + 2 * g) ^ ((r >> 1) & 7)) << 4;
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
       v[f].lo = *reinterpret_cast<const i32x4*>(&sh.b[b][rb0 + f * 32 * 128 + c0]);

@@ -307,11 +307,16 @@ __device__ __forceinline__ void store_quarter(const f32x16 (&acc)[FN][FM], uint8
   constexpr int kRow = quarter_bytes<FN, BF16>() / 32;
   constexpr int kLanes = 32 * FN * (BF16 ? 2 : 4) / 16, kEl = BF16 ? 8 : 4;   // lanes a row takes
   const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
+  float scale[FM];
+#pragma unroll
+  for (int fm = 0; fm < FM; ++fm) {
+    const int64_t m = m0 + fm * 32 + r;
+    scale[fm] = row_scale ? row_scale[m < row_end ? m : row_end - 1] : 1.0f;
+  }
 #pragma unroll
   for (int fm = 0; fm < FM; ++fm) {
     const int64_t mbase = m0 + fm * 32;
-    const int64_t m = mbase + r < row_end ? mbase + r : row_end - 1;
-    const float rs = row_scale ? row_scale[m] : 1.0f;
+    const float rs = scale[fm];
 #pragma unroll
     for (int fn = 0; fn < FN; ++fn)
 #pragma unroll

@@ -446,7 +446,8 @@ def fp8_matmul_tokblk(a, a_scales, b, b_scales, token_offsets, m, n, out_dtype=t
     """Per-expert weight gradient A_e [m, n_e] . B_e [n, n_e]^T -> [E, m, n].
 
     Operands as mxfp4_row_to_fp8_col_tokblk returns them (flat E4M3 columns and
-    flat fp32 scales) for hidden sizes m and n and the same token_offsets."""
+    flat fp32 scales) for hidden sizes m and n and the same token_offsets.  A
+    factor that the rows of b were used with (a_row_scale) has to be in a."""
     if stream is not None:
         return _on_stream(fp8_matmul_tokblk, locals())
     a, b = _codes(a), _codes(b)
@@ -479,7 +480,8 @@ def rmsnorm_quantize(x, weight, residual=None, eps=1e-6, fmt="fp8", q=None, scal
     fmt "mxfp4": q uint8 [.., cols/2], scales UE8M0 uint8 [.., cols/32]; "fp8":
     q E4M3 uint8 [.., cols], scales fp32 [.., cols/128].  The rows hold
     h * weight; row_scale (fp32, one per row) is 1 / rms, the a_row_scale of
-    the products.  Without a residual, and without an h to fill, h is x."""
+    the products, and a factor of dY's rows in the weight gradient.  Without a
+    residual, and without an h to fill, h is x."""
     if stream is not None:
         return _on_stream(rmsnorm_quantize, locals())
     shape, gpu, dt = x.shape, x.get_device(), x.dtype

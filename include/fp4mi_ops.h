@@ -80,6 +80,9 @@ int mxfp4_matmul_grouped(const void* a, int a_fmt, const void* a_scales, const f
  * columns dense per expert, power-of-two fp32 scales per channel and block of
  * 128 tokens).  For a layer Y = X . W^T with W[e] [M, N], A holds dY's columns
  * and B holds X's.  An expert without tokens gets zeros.
+ * No factor per token is applied: where Y took one (the products' a_row_scale
+ * r, so Y = diag(r) . X . W^T), dY's rows are multiplied by it before they are
+ * quantized.  dY's columns without it give another gradient, with no error.
  *
  *  a, b           bytes [T * M], [T * N], 4-byte aligned
  *  a_scales, b_scales  fp32 [M (ceil(T/128) + E)], [N (ceil(T/128) + E)],
@@ -102,11 +105,16 @@ int fp8_matmul_tokblk(const uint8_t* a, const float* a_scales, const uint8_t* b,
  *   z = fl32(h * weight), quantized to rows of format fmt (RTN).
  * The normalized row is row_scale * (codes * block scale): the factor that
  * depends on the whole row is kept apart as one fp32, for the products'
- * a_row_scale, so codes and block scales are those of z exactly.
+ * a_row_scale, so codes and block scales are those of z exactly.  The rows
+ * alone are not normalized: whatever reads them takes row_scale as a factor,
+ * the weight gradient by way of dY (fp8_matmul_tokblk; it reads columns, which
+ * are made from MXFP4 rows).
  *   MXFP4: as fp4_quantize.  FP8: the scale of 128 values is the least power
  *   of two 2^k, -126 <= k <= 127, with max|z| <= 448 * 2^k (2^-127 for a block
  *   of zeros), and the code is E4M3(z / 2^k), to nearest even, saturating.
- * Where h or z is infinite or NaN the row's outputs are unspecified.
+ * Where h or z is infinite or NaN the row's outputs are unspecified.  The sum
+ * of squares is taken in fp32: row_scale is 0 where it passes fp32's range (some
+ * |h| from 2^64), and squares below 2^-149 count as 0.
  *
  *  x, residual   [rows, cols] in dtype, 16-byte aligned; residual may be NULL
  *  weight        [cols] in weight_dtype, 16-byte aligned

@@ -16,7 +16,7 @@ namespace {
 // read once, by as many waves as there is work for, so that all of them are in
 // flight at once; splitting k inside the workgroup needs no second launch.  What
 // bounds it is the number of vector loads, then memory: 4096 x 7168 by one token
-// 4.8 us, 64 tokens over 32 experts of 2048 x 7168 29.5 us (4.8 TB/s).
+// 4.8 us, 64 tokens over 32 experts of 2048 x 7168 29.1 us (4.8 TB/s).
 template <bool A8>
 struct LaneStep {   // one lane's part of one 16-row operand at one step
   Frag<A8> v;
@@ -200,10 +200,10 @@ void launch_rows(ProductArgs p, int out_dtype, hipStream_t st) {
 // line-wide direct loads nor the 32-row fragment reads meet a bank twice (16
 // lanes of a read take all 64 banks: row parity picks the half, row / 2 the
 // place in it).
-// 8192^3 in 253 us, 4.3 PFLOP/s.  The matrix cores are busy 53% of the cycles,
+// 8192^3 in 255 us, 4.3 PFLOP/s.  The matrix cores are busy 55% of the cycles,
 // at the 1.8 GHz that the card holds under this load; each of a compute unit's 4
 // tiles has 10 us of start and output around it, and with the LDS reads, direct
-// loads and scales left out the rest takes 183 us in place of 253.
+// loads and scales left out the rest takes 183 us in place of 255.
 typedef __amdgpu_buffer_rsrc_t buffer_t;
 __device__ __forceinline__ buffer_t buffer_of(const void* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
@@ -536,7 +536,7 @@ __device__ __attribute__((noinline)) void rare_quarter(Fp8TileView v, int mw, in
 }
 
 // FP8 rows by MXFP4, see bf16_tile.  Two workgroups a compute unit hide each
-// other's starts and barriers (one: 227 us, two: 165 for 5001 tokens over 13
+// other's starts and barriers (one: 225 us, two: 159 for 5001 tokens over 13
 // experts of 7168 x 2048, 0.9 PFLOP/s).
 constexpr int kBM = 128;
 template <bool BF16>
@@ -593,17 +593,24 @@ void launch_fp8_tiles(ProductArgs p, int out_dtype, hipStream_t st) {
     launch_1d(product_fp8_tiles_kernel<false>, blocks, 256, st, p);
 }
 
-// Which kernel.  Up to 16 tokens: 16 x 16 a workgroup, the most workgroups (4096
-// x 7168 by one token: 5.4 us, 7.1 us with 32 x 32).  Then 32 x 32, whose time
-// follows the number of workgroups, until the tiles, whose time hardly depends
-// on it before the card is full, are faster (k = 4096; us, 32 x 32 | tiles):
-//   MXFP4 by workgroups of 32 x 32: 512: 13.5 | 19.5, 1024: 24.4 | 22.6,
-//   2048: 44.8 | 23.0; FP8: 1024: 44.6 | 72, 2048: 87 | 72.
-// Grouped, by tokens per shard (Zipf shards), where weights are read once a row
-// tile: MXFP4 16: 69 | 72, 32: 70 | 53; FP8 32: 69 | 73, 128: 204 | 77.
+// Which kernel.  The few-row kernels' time follows the number of workgroups; that
+// of the tiles hardly depends on it before the card is full.  So a plain product
+// goes by the number of 32 x 32 workgroups it would take (k = 4096; us, 32 x 32 |
+// tiles):
+//   MXFP4 512: 13.5 | 20.4, 1024: 24.1 | 22.2, 2048: 45.0 | 22.6;
+//   FP8 1024: 44.6 | 68, 2048: 87 | 68.
+// The count does not tell tokens from columns, and a wide weight takes tiles for
+// one token too (129280 x 7168; us, few-row | tiles): MXFP4 1 token 95 | 126, 32
+// tokens 139 | 130; FP8 213 | 194 and 272 | 201.
+// Below the tiles, up to 16 tokens take 16 x 16 a workgroup, the most workgroups
+// (4096 x 7168 by one token: 4.8 us, 6.8 us with 32 x 32).
+// Grouped, where weights are read once a row tile, by the mean of tokens a shard
+// (32 Zipf shards, 2048 x 4096): MXFP4 32: 69 | 53; FP8 32: 133 | 100, 128: 393 |
+// 112 (64 tokens by 2048 x 7168: 59 | 106).
 // Of the MXFP4 tiles, 256 x 128 keeps more compute units busy and 256 x 256 feeds
-// the matrix cores better: 256 tiles of the first 28.9 | 33.8, 512 55 | 44; with
-// shards under 256 tokens the second's rows stand empty (64 a shard: 55 | 69).
+// the matrix cores better (4096 x 4096; us, first | second): 2048 tokens, 256 tiles
+// of the first, 27.4 | 32.1; 4096 tokens 49.8 | 38.8.  With shards under 256 tokens
+// the second's rows stand empty (64 a shard: 86 | 102, 512 a shard: 261 | 209).
 template <bool A8, bool KT>
 void launch_product(const ProductArgs& p, int out_dtype, hipStream_t st) {
   const int64_t per = p.tokens / p.experts;

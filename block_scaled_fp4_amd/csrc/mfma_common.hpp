@@ -46,8 +46,10 @@ __device__ __forceinline__ f32x4 mfma_scaled(const Frag<false>& a, const Frag<fa
 // Products with an FP8 operand.  The scaled instruction lines the products of
 // adjacent k up with the largest of them and drops what lies 14 bits or more
 // below it; over E4M3's 18 binades that costs about 2e-5 of a sum (measured on
-// Gaussian rows), which is not a sum in fp32.  E2M1 by E2M1 spans 8 bits and
-// loses nothing, but E4M3 goes through bf16 products, which are exact and are
+// Gaussian rows), which is not a sum in fp32.  E2M1 by E2M1 spans 8 bits within
+// a block and loses nothing, whatever the other blocks' scales are (of a block
+// that cancels 2^0 to 2^40 above its neighbour the rest is 0.2 of fp32's last
+// place at most).  But E4M3 goes through bf16 products, which are exact and are
 // added in fp32 (6e-8 measured), at half the scaled instruction's rate.  A
 // lane then holds the 32 consecutive k from 32 g of both operands, and
 // instruction q of four takes its 8 from 8 q.
@@ -261,8 +263,9 @@ __device__ __forceinline__ void store_out4(void* out, int64_t row, int n_cols, i
 
 // 16 bytes at `src`: eight bf16 or four fp32 consecutive columns from n of one
 // output row; columns past the row's end are dropped.  Nontemporal: outputs of
-// whole tiles would push the operands out of the caches (the gradient of 16 x
-// 4096 x 7168: 1167 -> 1033 us, 8192^3 in MXFP4: 267 -> 256 us).
+// whole tiles would push the operands out of the caches (plain stores against
+// these: the gradient of 16 x 4096 x 7168 1100 | 1072 us, 5001 tokens by 13 x
+// 7168 x 2048 170 | 159 us, 8192^3 in MXFP4 260 | 256 us).
 template <bool BF16>
 __device__ __forceinline__ void store_chunk(void* out, int64_t row, int n_cols, int n,
                                             const uint8_t* src) {
@@ -455,9 +458,10 @@ __device__ __forceinline__ bool bf16_tile(Bf16Shared<A8, WM>& sh, int stages, in
     }
   };
   // before(i), i = 0 .. 7: ahead of the i-th eighth.  With E4M3 on both sides each
-  // eighth's fragments are read an eighth earlier (1098 -> 1041 us for 16 x 4096 x
-  // 7168); with E2M1 two workgroups share the registers and cover the reads, and
-  // the registers that this takes cost more (5001 tokens: 165 -> 177 us).
+  // eighth's fragments are read an eighth earlier (16 x 4096 x 7168: 1072 us, read
+  // in place 1086); with E2M1 two workgroups share the registers and cover the
+  // reads, and the registers that this takes cost more (5001 tokens by 13 x 7168 x
+  // 2048: in place 159 us, earlier 166).
   auto compute = [&](int s, auto before) {
     Frag<A8> va[2];
     Frag<true> vb[2];

@@ -97,24 +97,38 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream():
-    # torch.cuda.current_stream() without its Stream object, 0.3 us for 2.8
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+def _stream(stream):
+    if stream is None:   # torch.cuda.current_stream() without its Stream object, 0.3 us for 2.8
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
 def _on_stream(fn, args):
-    """fn(**args) with args["stream"] (a Stream or a raw handle) as the current
-    stream.  What fn allocates then comes from that stream's memory: a block
-    from another stream's could still be in use there, and scratch would go back
-    to it, for others to write, before the launches are done.  New outputs are
-    recorded on the caller's stream as well, where they are read."""
+    """fn(**args), which has something to allocate, with args["stream"] (a Stream
+    or a raw handle) as the current stream.  What fn allocates then comes from
+    that stream's memory: a block from another stream's could still be in use
+    there, and scratch would go back to it, for others to write, before the
+    launches are done.  New outputs are recorded on the caller's stream as well,
+    where they are read."""
     stream = args.pop("stream")
     if not isinstance(stream, torch.cuda.Stream):
         handle = getattr(stream, "cuda_stream", stream)
-        stream = torch.cuda.ExternalStream(getattr(handle, "value", handle) or 0)
-    caller = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
+        handle = getattr(handle, "value", handle) or 0
+        if handle == _stream(None):
+            return fn(**args)
+        stream = torch.cuda.ExternalStream(handle)
+    elif stream.cuda_stream == _stream(None):
+        return fn(**args)
+    before = caller = torch.cuda.current_stream()
+    if stream.device != before.device:   # a stream of another GPU: that one's current stream
+        caller = torch.cuda.current_stream(stream.device)
+    torch.cuda.set_stream(stream)
+    try:
         out = fn(**args)
+    finally:
+        if caller is not before:
+            torch.cuda.set_stream(caller)
+        torch.cuda.set_stream(before)
     for t in out if isinstance(out, tuple) else (out,):
         if t is not None and not any(t is a for a in args.values()):
             t.record_stream(caller)
@@ -156,7 +170,7 @@ def fp4_quantize(x, fmt="nvfp4", rounding="rtn", seed=0, step=0, tscale="compute
                  tensor_scale=None, packed=None, scales=None, stream=None):
     """Quantize x [.., cols] -> (packed uint8 [rows, cols/2], scales uint8, tensor_scale).
     tensor_scale is a 1-element fp32 device tensor (NVFP4; None for MXFP4)."""
-    if stream is not None:
+    if stream is not None and (packed is None or scales is None or (tensor_scale is None and fmt == "nvfp4")):
         return _on_stream(fp4_quantize, locals())
     _dev(x)
     cols = x.shape[-1]
@@ -173,14 +187,14 @@ def fp4_quantize(x, fmt="nvfp4", rounding="rtn", seed=0, step=0, tscale="compute
     _arg(tensor_scale, "tensor_scale", torch.float32, 1, x.device, optional=fmt == "mxfp4")
     _check("fp4_quantize", _lib.fp4_quantize(
         _ptr(x), _dtype_code(x.dtype), rows, cols, FMT[fmt], ROUND[rounding], seed, step,
-        TSCALE[tscale], _ptr(tensor_scale), _ptr(packed), _ptr(scales), _stream()))
+        TSCALE[tscale], _ptr(tensor_scale), _ptr(packed), _ptr(scales), _stream(stream)))
     return packed, scales, tensor_scale
 
 
 def fp4_dequantize(packed, scales, rows, cols, fmt="nvfp4", tensor_scale=None,
                    out_dtype=torch.bfloat16, y=None, stream=None):
     """Receiver: (packed, scales[, tensor_scale]) -> y [rows, cols] in out_dtype."""
-    if stream is not None:
+    if stream is not None and y is None:
         return _on_stream(fp4_dequantize, locals())
     _dev(packed)
     if y is None:
@@ -192,27 +206,28 @@ def fp4_dequantize(packed, scales, rows, cols, fmt="nvfp4", tensor_scale=None,
     _arg(y, "y", y.dtype, rows * cols, packed.device)
     _check("fp4_dequantize", _lib.fp4_dequantize(
         _ptr(packed), _ptr(scales), _ptr(tensor_scale), rows, cols, FMT[fmt], _ptr(y),
-        _dtype_code(y.dtype), _stream()))
+        _dtype_code(y.dtype), _stream(stream)))
     return y
 
 
 def fp4quant_encode(x, group, packed=None, s_rms=None, s_abs=None, stream=None):
     """FP4Quant encode -> (packed [rows, cols/2], s_rms [rows, cols/G], s_abs [rows, cols/G])."""
-    if stream is not None:
+    if stream is not None and (packed is None or s_rms is None or s_abs is None):
         return _on_stream(fp4quant_encode, locals())
-    return _fq_encode("fp4quant_encode", x, group, None, 0, 0, packed, s_rms, s_abs)
+    return _fq_encode("fp4quant_encode", x, group, None, 0, 0, packed, s_rms, s_abs, stream)
 
 
 def fp4quant_encode_ex(x, group, rounding="sr", seed=0, step=0, packed=None, s_rms=None, s_abs=None,
                        stream=None):
     """FP4Quant encode with RTN or stochastic rounding keyed by (seed, step,
     element index) -> (packed, s_rms, s_abs) as fp4quant_encode."""
-    if stream is not None:
+    if stream is not None and (packed is None or s_rms is None or s_abs is None):
         return _on_stream(fp4quant_encode_ex, locals())
-    return _fq_encode("fp4quant_encode_ex", x, group, rounding, seed, step, packed, s_rms, s_abs)
+    return _fq_encode("fp4quant_encode_ex", x, group, rounding, seed, step, packed, s_rms, s_abs,
+                      stream)
 
 
-def _fq_encode(fn, x, group, rounding, seed, step, packed, s_rms, s_abs):
+def _fq_encode(fn, x, group, rounding, seed, step, packed, s_rms, s_abs, stream):
     _dev(x)
     cols = x.shape[-1]
     rows = x.numel() // cols if cols else 0
@@ -228,11 +243,11 @@ def _fq_encode(fn, x, group, rounding, seed, step, packed, s_rms, s_abs):
     _arg(s_abs, "s_abs", torch.float32, rows * ng, x.device)
     if rounding is None:
         status = _lib.fp4quant_encode(_ptr(x), _dtype_code(x.dtype), rows, cols, group, _ptr(packed),
-                                      _ptr(s_rms), _ptr(s_abs), _stream())
+                                      _ptr(s_rms), _ptr(s_abs), _stream(stream))
     else:
         status = _lib.fp4quant_encode_ex(_ptr(x), _dtype_code(x.dtype), rows, cols, group,
                                          ROUND.get(rounding, 99), seed, step, _ptr(packed), _ptr(s_rms),
-                                         _ptr(s_abs), _stream())
+                                         _ptr(s_abs), _stream(stream))
     _check(fn, status)
     return packed, s_rms, s_abs
 
@@ -240,7 +255,7 @@ def _fq_encode(fn, x, group, rounding, seed, step, packed, s_rms, s_abs):
 def fp4quant_decode(packed, s_rms, s_abs, rows, cols, group, out_dtype=torch.bfloat16, y=None,
                     stream=None):
     """FP4Quant receiver -> y [rows, cols]."""
-    if stream is not None:
+    if stream is not None and y is None:
         return _on_stream(fp4quant_decode, locals())
     _dev(packed)
     if y is None:
@@ -252,7 +267,7 @@ def fp4quant_decode(packed, s_rms, s_abs, rows, cols, group, out_dtype=torch.bfl
     _arg(y, "y", y.dtype, rows * cols, packed.device)
     _check("fp4quant_decode", _lib.fp4quant_decode(
         _ptr(packed), _ptr(s_rms), _ptr(s_abs), rows, cols, group, _ptr(y), _dtype_code(y.dtype),
-        _stream()))
+        _stream(stream)))
     return y
 
 
@@ -261,7 +276,7 @@ def fp4_errfeedback_qdq(x, residual=None, y=None, out_dtype=None, rounding="sr",
                         stream=None):
     """NVFP4 qdq with an fp32 error-feedback residual (updated in place).
     Returns (y, tensor_scale).  y may be x for an in-place update."""
-    if stream is not None:
+    if stream is not None and (y is None or tensor_scale is None):
         return _on_stream(fp4_errfeedback_qdq, locals())
     _dev(x)
     cols = x.shape[-1]
@@ -279,7 +294,7 @@ def fp4_errfeedback_qdq(x, residual=None, y=None, out_dtype=None, rounding="sr",
     _check("fp4_errfeedback_qdq", _lib.fp4_errfeedback_qdq(
         _ptr(x), _dtype_code(x.dtype), rows, cols, _ptr(residual), _ptr(y), _dtype_code(y.dtype),
         ROUND[rounding], seed, step, TSCALE[tscale], _ptr(tensor_scale), _ptr(packed),
-        _ptr(scales), _stream()))
+        _ptr(scales), _stream(stream)))
     return y, tensor_scale
 
 
@@ -287,7 +302,7 @@ def mxfp4_row_to_fp8_col(packed, scales_e8m0, token_offsets, hidden, fp8_out=Non
                          fp8_scales=None, stream=None):
     """Ragged MXFP4 rows [T, H/2] (+ UE8M0 [T, H/32]) -> per-expert FP8 E4M3
     columns (flat uint8 [T*H]) and fp32 block scales (flat [T*H/128])."""
-    if stream is not None:
+    if stream is not None and (fp8_out is None or fp8_scales is None):
         return _on_stream(mxfp4_row_to_fp8_col, locals())
     _dev(packed)
     T = packed.shape[0]
@@ -303,7 +318,7 @@ def mxfp4_row_to_fp8_col(packed, scales_e8m0, token_offsets, hidden, fp8_out=Non
     _arg(fp8_scales, "fp8_scales", torch.float32, T * hidden // 128, packed.device)
     _check("mxfp4_row_to_fp8_col", _lib.mxfp4_row_to_fp8_col(
         _ptr(packed), _ptr(scales_e8m0), _ptr(token_offsets), E, T, hidden, _ptr(fp8_out),
-        _ptr(fp8_scales), _stream()))
+        _ptr(fp8_scales), _stream(stream)))
     return fp8_out, fp8_scales
 
 
@@ -318,7 +333,7 @@ def mxfp4_row_to_fp8_col_tokblk(packed, scales_e8m0, token_offsets, hidden, fp8_
     columns (flat uint8 [T*H]) with FP8 blocks of 128 tokens per channel, and
     fp32 scales (flat [H (ceil(T/128) + E)]; expert e's [H, ceil(n_e/128)]
     matrix at element H (ceil(off_e/128) + e))."""
-    if stream is not None:
+    if stream is not None and (fp8_out is None or fp8_scales is None):
         return _on_stream(mxfp4_row_to_fp8_col_tokblk, locals())
     _dev(packed)
     T = packed.shape[0]
@@ -335,7 +350,7 @@ def mxfp4_row_to_fp8_col_tokblk(packed, scales_e8m0, token_offsets, hidden, fp8_
     _arg(fp8_scales, "fp8_scales", torch.float32, nsc, packed.device)
     _check("mxfp4_row_to_fp8_col_tokblk", _lib.mxfp4_row_to_fp8_col_tokblk(
         _ptr(packed), _ptr(scales_e8m0), _ptr(token_offsets), E, T, hidden, _ptr(fp8_out),
-        _ptr(fp8_scales), _stream()))
+        _ptr(fp8_scales), _stream(stream)))
     return fp8_out, fp8_scales
 
 
@@ -343,7 +358,7 @@ def mxfp4_row_to_fp8_row(packed, scales_e8m0, hidden, fp8_out=None, fp8_scales=N
                          stream=None):
     """MXFP4 rows [T, H/2] (+ UE8M0 [T, H/32]) -> FP8 E4M3 rows [T, H] and
     fp32 block scales [T, H/128] (no transpose)."""
-    if stream is not None:
+    if stream is not None and (fp8_out is None or fp8_scales is None):
         return _on_stream(mxfp4_row_to_fp8_row, locals())
     _dev(packed)
     T = packed.shape[0]
@@ -357,7 +372,7 @@ def mxfp4_row_to_fp8_row(packed, scales_e8m0, hidden, fp8_out=None, fp8_scales=N
     _arg(fp8_scales, "fp8_scales", torch.float32, T * hidden // 128, packed.device)
     _check("mxfp4_row_to_fp8_row", _lib.mxfp4_row_to_fp8_row(
         _ptr(packed), _ptr(scales_e8m0), T, hidden, _ptr(fp8_out), _ptr(fp8_scales),
-        _stream()))
+        _stream(stream)))
     return fp8_out, fp8_scales
 
 
@@ -371,7 +386,7 @@ def _codes(t):
     return t.view(torch.uint8) if t.dtype is torch.float8_e4m3fn else t
 
 
-def _product(name, a, a_scales, a_row_scale, w, w_scales, offsets, out_dtype, out):
+def _product(name, a, a_scales, a_row_scale, w, w_scales, offsets, out_dtype, out, stream):
     """Checks and launches either product (small sizes are over in the time
     that a call takes here, so the common case is one run of plain tests)."""
     a = _codes(a)
@@ -403,11 +418,11 @@ def _product(name, a, a_scales, a_row_scale, w, w_scales, offsets, out_dtype, ou
     if offsets is None:
         status = _lib.mxfp4_matmul(a.data_ptr(), fp8, a_scales.data_ptr(), row, w.data_ptr(),
                                    w_scales.data_ptr(), M, N, K, out.data_ptr(),
-                                   _dtype_code(out.dtype), _stream())
+                                   _dtype_code(out.dtype), _stream(stream))
     else:
         status = _lib.mxfp4_matmul_grouped(a.data_ptr(), fp8, a_scales.data_ptr(), row, w.data_ptr(),
                                            w_scales.data_ptr(), offsets.data_ptr(), E, M, N, K,
-                                           out.data_ptr(), _dtype_code(out.dtype), _stream())
+                                           out.data_ptr(), _dtype_code(out.dtype), _stream(stream))
     _check(name, status)
     return out
 
@@ -420,25 +435,25 @@ def mxfp4_matmul(a, a_scales, b, b_scales, a_row_scale=None, out_dtype=torch.bfl
     [.., K], uint8 or float8_e4m3fn, with power-of-two fp32 scales [.., K/128]):
     the scales' dtype tells.  b is MXFP4 [N, K/2].  a_row_scale: fp32 factor
     per row of a, such as rmsnorm_quantize's row_scale."""
-    if stream is not None:
+    if stream is not None and out is None:
         return _on_stream(mxfp4_matmul, locals())
     if b.dim() != 2:
         raise ValueError("b must be [N, K/2]")
-    return _product("mxfp4_matmul", a, a_scales, a_row_scale, b, b_scales, None, out_dtype, out)
+    return _product("mxfp4_matmul", a, a_scales, a_row_scale, b, b_scales, None, out_dtype, out, stream)
 
 
 def mxfp4_matmul_grouped(a, a_scales, w, w_scales, token_offsets, a_row_scale=None,
                          out_dtype=torch.bfloat16, out=None, stream=None):
     """Rows token_offsets[e] .. token_offsets[e+1]-1 of a [T, K] times w[e]^T,
     w MXFP4 [E, N, K/2] -> [T, N].  Operands as mxfp4_matmul."""
-    if stream is not None:
+    if stream is not None and out is None:
         return _on_stream(mxfp4_matmul_grouped, locals())
     if w.dim() != 3:
         raise ValueError("w must be [E, N, K/2]")
     if token_offsets is None:
         raise ValueError("token_offsets is required")
     return _product("mxfp4_matmul_grouped", a, a_scales, a_row_scale, w, w_scales, token_offsets,
-                    out_dtype, out)
+                    out_dtype, out, stream)
 
 
 def fp8_matmul_tokblk(a, a_scales, b, b_scales, token_offsets, m, n, out_dtype=torch.bfloat16,
@@ -448,7 +463,7 @@ def fp8_matmul_tokblk(a, a_scales, b, b_scales, token_offsets, m, n, out_dtype=t
     Operands as mxfp4_row_to_fp8_col_tokblk returns them (flat E4M3 columns and
     flat fp32 scales) for hidden sizes m and n and the same token_offsets.  A
     factor that the rows of b were used with (a_row_scale) has to be in a."""
-    if stream is not None:
+    if stream is not None and out is None:
         return _on_stream(fp8_matmul_tokblk, locals())
     a, b = _codes(a), _codes(b)
     gpu, T, E = a.get_device(), a.numel() // m if m else 0, token_offsets.numel() - 1
@@ -468,7 +483,7 @@ def fp8_matmul_tokblk(a, a_scales, b, b_scales, token_offsets, m, n, out_dtype=t
     _check("fp8_matmul_tokblk", _lib.fp8_matmul_tokblk(
         a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(),
         token_offsets.data_ptr(), E, T, m, n, out.data_ptr(), _dtype_code(out.dtype),
-        _stream()))
+        _stream(stream)))
     return out
 
 
@@ -482,7 +497,8 @@ def rmsnorm_quantize(x, weight, residual=None, eps=1e-6, fmt="fp8", q=None, scal
     h * weight; row_scale (fp32, one per row) is 1 / rms, the a_row_scale of
     the products, and a factor of dY's rows in the weight gradient.  Without a
     residual, and without an h to fill, h is x."""
-    if stream is not None:
+    if stream is not None and (q is None or scales is None or row_scale is None or
+                               (h is None and residual is not None)):
         return _on_stream(rmsnorm_quantize, locals())
     shape, gpu, dt = x.shape, x.get_device(), x.dtype
     cols = shape[-1]
@@ -513,7 +529,7 @@ def rmsnorm_quantize(x, weight, residual=None, eps=1e-6, fmt="fp8", q=None, scal
     _check("rmsnorm_quantize", _lib.rmsnorm_quantize(
         x.data_ptr(), _ptr(residual), _dtype_code(dt), weight.data_ptr(), _dtype_code(weight.dtype),
         rows, cols, eps, ROWS.get(fmt, 99), q.data_ptr(), scales.data_ptr(), row_scale.data_ptr(),
-        _ptr(h), _stream()))
+        _ptr(h), _stream(stream)))
     return q, scales, row_scale, x if h is None else h
 
 
@@ -522,7 +538,7 @@ def rmsnorm_backward(dy, h, weight, row_scale, dh=None, dx=None, dweight=None, w
     """Gradient of row_scale * h * weight -> (dx, dweight fp32 [cols]); dh, if
     given, is added to dx.  workspace: uint8 of at least
     rmsnorm_backward_workspace(rows, cols) elements (allocated if None)."""
-    if stream is not None:
+    if stream is not None and (dx is None or dweight is None or workspace is None):
         return _on_stream(rmsnorm_backward, locals())
     gpu, dt, cols = dy.get_device(), dy.dtype, dy.shape[-1]
     rows = dy.numel() // cols if cols else 0
@@ -548,7 +564,7 @@ def rmsnorm_backward(dy, h, weight, row_scale, dh=None, dx=None, dweight=None, w
     _check("rmsnorm_backward", _lib.rmsnorm_backward(
         dy.data_ptr(), h.data_ptr(), _ptr(dh), _dtype_code(dt), weight.data_ptr(),
         _dtype_code(weight.dtype), row_scale.data_ptr(), rows, cols, dx.data_ptr(),
-        dweight.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream()))
+        dweight.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)))
     return dx, dweight
 
 

@@ -8,7 +8,6 @@ the kernels run.  Here (CPU) the library is a stub, tensors are fake, and the
 current stream is a variable: each allocation is logged with it.  On the GPU
 the same calls run behind a delayed stream, with the caller's stream taking
 and filling blocks of the same sizes meanwhile."""
-import contextlib
 import ctypes
 
 import numpy as np
@@ -63,11 +62,8 @@ def fake_gpu(monkeypatch):
     log = {"new": [], "launch": [], "recorded": {}}
     current = [FakeStream(1)]
 
-    @contextlib.contextmanager
-    def stream(s):
-        current.append(s)
-        yield
-        current.pop()
+    def set_stream(s):
+        current[0] = s
 
     class Stub:
         def __getattr__(self, name):
@@ -81,16 +77,16 @@ def fake_gpu(monkeypatch):
     class Allocations(TorchDispatchMode):
         def __torch_dispatch__(self, func, types, args=(), kwargs=None):
             if "empty" in str(func):
-                log["new"].append(current[-1].cuda_stream)
+                log["new"].append(current[0].cuda_stream)
             return func(*args, **(kwargs or {}))
 
     monkeypatch.setattr(m, "_lib", Stub())
     monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", FakeStream)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[-1])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[0])
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(torch.cuda, "stream", stream)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: current[-1].cuda_stream, raising=False)
+    monkeypatch.setattr(torch.cuda, "set_stream", set_stream)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: current[0].cuda_stream, raising=False)
     monkeypatch.setattr(torch.Tensor, "data_ptr", lambda t: 4096)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: log["recorded"].update({id(t): s.cuda_stream}))
     return log, Allocations
@@ -134,6 +130,34 @@ def _gpu_inputs(seed):
             return torch.ones(shape, device="cuda")
         return torch.randn(shape, generator=g, device="cuda").to(dt)
     return t
+
+
+def test_nothing_to_allocate(fake_gpu):
+    """Outputs given: the launch goes to the stream, and nothing else happens."""
+    log, allocations = fake_gpu
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        t = lambda dt, *shape: torch.empty(shape, dtype=dt, device="cuda:0")
+        x, q, s, f = t(torch.bfloat16, T, H), t(torch.uint8, T, H // 2), t(torch.uint8, T, H // 32), t(torch.float32, T)
+        g, o8, s8, o = t(torch.float32, H), t(torch.uint8, T, H), t(torch.float32, T, 2), t(torch.bfloat16, T, T)
+        ws = t(torch.uint8, 4096)
+        with allocations():
+            m.fp4_quantize(x, "mxfp4", packed=q, scales=s, stream=2)
+            m.fp4_dequantize(q, s, T, H, "mxfp4", y=x, stream=FakeStream(2))
+            m.mxfp4_row_to_fp8_row(q, s, H, o8, s8, stream=2)
+            m.mxfp4_matmul(q, s, q, s, out=o, stream=2)
+            m.rmsnorm_quantize(x, g, fmt="mxfp4", q=q, scales=s, row_scale=f, stream=2)
+            m.rmsnorm_backward(x, x, g, f, dx=x, dweight=g, workspace=ws, stream=2)
+    assert log["launch"] == [2] * 6 and not log["new"] and not log["recorded"]
+
+
+def test_an_error_leaves_the_current_stream(fake_gpu):
+    log, _ = fake_gpu
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        x = torch.empty((T, H), dtype=torch.bfloat16, device="cuda:0")
+        with pytest.raises(ValueError):
+            m.rmsnorm_quantize(x, torch.empty(H - 1, device="cuda:0"), stream=2)
+        m.rmsnorm_quantize(x, torch.empty(H, device="cuda:0"))
+    assert log["launch"] == [1]
 
 
 @pytest.mark.gpu

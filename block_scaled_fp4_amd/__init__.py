@@ -14,6 +14,9 @@ Entry points (same names as the C ABI in include/fp4mi.h):
 and in include/fp4mi_ops.h:
   mxfp4_matmul, mxfp4_matmul_grouped, fp8_matmul_tokblk, rmsnorm_quantize,
   rmsnorm_backward
+and in include/fp4mi_moe.h:
+  fp8_quantize, fp8_quantize_blocks, fp8_matmul, fp8_matmul_grouped,
+  swiglu_quantize, swiglu_backward, router_balance, router_balance_backward
 plus ErrorFeedback, a name-keyed holder of residual buffers in the style of
 the fp4-train page's ErrorFeedback.qdq(name, x, step).
 """
@@ -56,6 +59,14 @@ _SIGS = {
     "fp8_matmul_tokblk": [_p, _p, _p, _p, _p, _i32, _i64, _i64, _i64, _p, _i, _p],
     "rmsnorm_quantize": [_p, _p, _i, _p, _i, _i64, _i64, _f, _i, _p, _p, _p, _p, _p],
     "rmsnorm_backward": [_p, _p, _p, _i, _p, _i, _p, _i64, _i64, _p, _p, _p, _i64, _p],
+    "fp8_quantize": [_p, _i, _i64, _i64, _p, _p, _p],
+    "fp8_quantize_blocks": [_p, _i, _i64, _i64, _i64, _p, _p, _p, _p, _p],
+    "fp8_matmul": [_p, _p, _p, _p, _p, _i, _i64, _i64, _i64, _p, _i, _p],
+    "fp8_matmul_grouped": [_p, _p, _p, _p, _p, _i, _p, _i32, _i64, _i64, _i64, _p, _i, _p],
+    "swiglu_quantize": [_p, _i, _i64, _i64, _i, _p, _p, _p, _p, _p],
+    "swiglu_backward": [_p, _i, _p, _p, _i64, _i64, _p, _i, _p, _p, _p],
+    "router_balance": [_p, _i, _p, _i, _p, _i64, _i32, _i32, _f, _p, _p, _p, _p, _p, _i64, _p],
+    "router_balance_backward": [_p, _i, _p, _p, _p, _p, _i64, _i32, _p, _p],
 }
 for _name, _args in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -63,6 +74,8 @@ for _name, _args in _SIGS.items():
     _fn.restype = ctypes.c_int
 _lib.rmsnorm_backward_workspace.argtypes = [_i64, _i64]
 _lib.rmsnorm_backward_workspace.restype = ctypes.c_int64
+_lib.router_balance_workspace.argtypes = [_i64, _i32]
+_lib.router_balance_workspace.restype = ctypes.c_int64
 _lib.fp4_status_string.argtypes = [ctypes.c_int]
 _lib.fp4_status_string.restype = ctypes.c_char_p
 _lib.fp4_abi_version.argtypes = []
@@ -101,6 +114,14 @@ def _stream(stream):
     if stream is None:   # torch.cuda.current_stream() without its Stream object, 0.3 us for 2.8
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _stream_on(gpu, stream):
+    """_stream(stream) for tensors on GPU number `gpu`, which has to be the current
+    one: a launch goes to the current GPU, whatever its pointers are."""
+    if gpu != torch.cuda.current_device():
+        raise ValueError(f"tensors are on GPU {gpu}, which is not the current one")
+    return _stream(stream)
 
 
 def _on_stream(fn, args):
@@ -571,6 +592,317 @@ def rmsnorm_backward(dy, h, weight, row_scale, dh=None, dx=None, dweight=None, w
 def rmsnorm_backward_workspace(rows, cols):
     """Bytes of rmsnorm_backward's workspace."""
     return _lib.rmsnorm_backward_workspace(rows, cols)
+
+
+def fp8_quantize(x, q=None, scales=None, stream=None):
+    """x [.., cols] in FP8 rows -> (q E4M3 uint8 [.., cols], scales fp32 [.., cols/128]):
+    a power of two for 128 values, as the products read them."""
+    if stream is not None and (q is None or scales is None):
+        return _on_stream(fp8_quantize, locals())
+    shape, gpu = x.shape, x.get_device()
+    cols = shape[-1]
+    rows = x.numel() // cols if cols else 0
+    n = rows * cols
+    if q is None:
+        q = torch.empty_like(x, dtype=torch.uint8)
+    else:
+        q = _codes(q)
+    if scales is None:
+        scales = x.new_empty((*shape[:-1], cols // 128), dtype=torch.float32)
+    if not (gpu >= 0 and _fits(x, x.dtype, n, gpu) and _fits(q, torch.uint8, n, gpu)
+            and _fits(scales, torch.float32, n // 128, gpu)):
+        _dev(x)
+        _arg(q, "q", torch.uint8, n, x.device)
+        _arg(scales, "scales", torch.float32, n // 128, x.device)
+    _check("fp8_quantize", _lib.fp8_quantize(
+        x.data_ptr(), _dtype_code(x.dtype), rows, cols, q.data_ptr(), scales.data_ptr(), _stream_on(gpu, stream)))
+    return q, scales
+
+
+def fp8_quantize_blocks(x, transposed=False, q=None, scales=None, q_t=None, scales_t=None, stream=None):
+    """x [.., rows, cols] in FP8 blocks of 128 x 128 -> (q E4M3 uint8 of x's shape,
+    scales fp32 [.., ceil(rows/128), cols/128], q_t, scales_t).
+
+    transposed=True (or q_t and scales_t given; rows % 128 == 0): q_t uint8
+    [.., cols, rows] holds the same codes transposed, scales_t [.., cols/128,
+    rows/128]; else both are None."""
+    transposed = transposed or q_t is not None or scales_t is not None
+    if stream is not None and (q is None or scales is None or (transposed and (q_t is None or scales_t is None))):
+        return _on_stream(fp8_quantize_blocks, locals())
+    _dev(x)
+    if x.dim() < 2:
+        raise ValueError("x must be [.., rows, cols]")
+    gpu = x.get_device()
+    (rows, cols), lead = x.shape[-2:], x.shape[:-2]
+    n = x.numel()
+    batch = n // (rows * cols) if n else 0
+    row_tiles, col_tiles = (rows + 127) // 128, cols // 128
+    if q is None:
+        q = torch.empty_like(x, dtype=torch.uint8)
+    if scales is None:
+        scales = x.new_empty((*lead, row_tiles, col_tiles), dtype=torch.float32)
+    if transposed and q_t is None:
+        q_t = x.new_empty((*lead, cols, rows), dtype=torch.uint8)
+    if transposed and scales_t is None:
+        scales_t = x.new_empty((*lead, col_tiles, row_tiles), dtype=torch.float32)
+    q = _codes(q)
+    q_t = _codes(q_t) if transposed else None
+    tiles = batch * row_tiles * col_tiles
+    _arg(q, "q", torch.uint8, n, x.device)
+    _arg(scales, "scales", torch.float32, tiles, x.device)
+    _arg(q_t, "q_t", torch.uint8, n, x.device, optional=True)
+    _arg(scales_t, "scales_t", torch.float32, tiles, x.device, optional=True)
+    _check("fp8_quantize_blocks", _lib.fp8_quantize_blocks(
+        x.data_ptr(), _dtype_code(x.dtype), batch, rows, cols, q.data_ptr(), scales.data_ptr(),
+        _ptr(q_t), _ptr(scales_t), _stream_on(gpu, stream)))
+    return q, scales, q_t, scales_t
+
+
+def _fp8_product(name, a, a_scales, a_row_scale, w, w_scales, offsets, out_dtype, out, stream):
+    """Checks and launches either product of FP8 by FP8."""
+    a, w = _codes(a), _codes(w)
+    shape, gpu = a.shape, a.get_device()
+    K, N, E = shape[-1], w.shape[-2], 1 if offsets is None else w.shape[0]
+    M = a.numel() // K if K else 0
+    if w.shape[-1] != K:
+        raise ValueError(f"a has {K} columns, the weights have {w.shape[-1]}")
+    srows = w_scales.shape[-2] if w_scales.dim() > 1 else -1
+    if srows not in (N, (N + 127) // 128):
+        raise ValueError(f"the weights' scales must have {N} rows or {(N + 127) // 128} rows of blocks")
+    if out is None:
+        out = a.new_empty((M, N) if len(shape) == 2 else (*shape[:-1], N), dtype=out_dtype)
+    ns, nws = M * (K // 128), E * srows * (K // 128)
+    if not (gpu >= 0 and _fits(a, torch.uint8, M * K, gpu) and _fits(a_scales, torch.float32, ns, gpu)
+            and _fits(w, torch.uint8, E * N * K, gpu) and _fits(w_scales, torch.float32, nws, gpu)
+            and _fits(out, out.dtype, M * N, gpu)
+            and (a_row_scale is None or _fits(a_row_scale, torch.float32, M, gpu))
+            and (offsets is None or _fits(offsets, torch.int64, E + 1, gpu))):
+        _dev(a)
+        _arg(a, "a", torch.uint8, M * K, a.device)
+        _arg(a_scales, "a_scales", torch.float32, ns, a.device)
+        _arg(w, "w", torch.uint8, E * N * K, a.device)
+        _arg(w_scales, "w_scales", torch.float32, nws, a.device)
+        _arg(out, "out", out.dtype, M * N, a.device)
+        _arg(a_row_scale, "a_row_scale", torch.float32, M, a.device, optional=True)
+        _arg(offsets, "token_offsets", torch.int64, E + 1, a.device, optional=True)
+    row = None if a_row_scale is None else a_row_scale.data_ptr()
+    block = 1 if srows == N else 128
+    if offsets is None:
+        status = _lib.fp8_matmul(a.data_ptr(), a_scales.data_ptr(), row, w.data_ptr(), w_scales.data_ptr(),
+                                 block, M, N, K, out.data_ptr(), _dtype_code(out.dtype), _stream_on(gpu, stream))
+    else:
+        status = _lib.fp8_matmul_grouped(a.data_ptr(), a_scales.data_ptr(), row, w.data_ptr(),
+                                         w_scales.data_ptr(), block, offsets.data_ptr(), E, M, N, K,
+                                         out.data_ptr(), _dtype_code(out.dtype), _stream_on(gpu, stream))
+    _check(name, status)
+    return out
+
+
+def fp8_matmul(a, a_scales, b, b_scales, a_row_scale=None, out_dtype=torch.bfloat16, out=None,
+               stream=None):
+    """a [.., K] . b [N, K]^T -> [.., N] in out_dtype (or out's dtype).
+
+    a in FP8 rows (E4M3, uint8 or float8_e4m3fn, with power-of-two fp32 scales
+    [.., K/128]), b with scales [N, K/128] (FP8 rows) or [ceil(N/128), K/128] (FP8
+    blocks).  a_row_scale: fp32 factor per row of a.  fp32 outputs are sums of
+    exact products; for bf16 outputs products far below their neighbours along K
+    are dropped (2e-5 of a sum of Gaussian values)."""
+    if stream is not None and out is None:
+        return _on_stream(fp8_matmul, locals())
+    if b.dim() != 2:
+        raise ValueError("b must be [N, K]")
+    return _fp8_product("fp8_matmul", a, a_scales, a_row_scale, b, b_scales, None, out_dtype, out, stream)
+
+
+def fp8_matmul_grouped(a, a_scales, w, w_scales, token_offsets, a_row_scale=None,
+                       out_dtype=torch.bfloat16, out=None, stream=None):
+    """Rows token_offsets[e] .. token_offsets[e+1]-1 of a [T, K] times w[e]^T,
+    w [E, N, K] with scales [E, N, K/128] or [E, ceil(N/128), K/128] -> [T, N].
+    Operands as fp8_matmul."""
+    if stream is not None and out is None:
+        return _on_stream(fp8_matmul_grouped, locals())
+    if w.dim() != 3 or w_scales.dim() != 3:
+        raise ValueError("w and w_scales must be [E, .., ..]")
+    if token_offsets is None:
+        raise ValueError("token_offsets is required")
+    return _fp8_product("fp8_matmul_grouped", a, a_scales, a_row_scale, w, w_scales, token_offsets,
+                        out_dtype, out, stream)
+
+
+def swiglu_quantize(x, fmt="fp8", checkpoint=True, q=None, scales=None, ckpt=None, ckpt_scales=None,
+                    stream=None):
+    """silu(g) * u of x = [g | u] [.., 2 ffn] as quantized rows, with an FP8
+    checkpoint of x -> (q, scales, ckpt, ckpt_scales).
+
+    fmt "mxfp4": q uint8 [.., ffn/2], scales UE8M0 uint8 [.., ffn/32]; "fp8": q E4M3
+    uint8 [.., ffn], scales fp32 [.., ffn/128].  ckpt: E4M3 uint8 [.., 2 ffn] with
+    ckpt_scales fp32 [.., 2 ffn/128], for swiglu_backward; both None with
+    checkpoint=False (unless they are given)."""
+    checkpoint = checkpoint or ckpt is not None or ckpt_scales is not None
+    if stream is not None and (q is None or scales is None or (checkpoint and (ckpt is None or ckpt_scales is None))):
+        return _on_stream(swiglu_quantize, locals())
+    shape, gpu, dt = x.shape, x.get_device(), x.dtype
+    width, lead = shape[-1], shape[:-1]
+    if width % 2:
+        raise ValueError("x must be [.., 2 ffn]")
+    ffn = width // 2
+    rows = x.numel() // width if width else 0
+    fp8 = fmt == "fp8"
+    per, block, sdt = (1, 128, torch.float32) if fp8 else (2, 32, torch.uint8)
+    if q is None:
+        q = x.new_empty((*lead, ffn // per), dtype=torch.uint8)
+    if scales is None:
+        scales = x.new_empty((*lead, ffn // block), dtype=sdt)
+    if checkpoint and ckpt is None:
+        ckpt = torch.empty_like(x, dtype=torch.uint8)
+    if checkpoint and ckpt_scales is None:
+        ckpt_scales = x.new_empty((*lead, width // 128), dtype=torch.float32)
+    q = _codes(q)
+    n = rows * ffn
+    if checkpoint:
+        ckpt = _codes(ckpt)
+    if not (gpu >= 0 and _fits(x, dt, 2 * n, gpu) and _fits(q, torch.uint8, n // per, gpu)
+            and _fits(scales, sdt, n // block, gpu)
+            and (not checkpoint or (_fits(ckpt, torch.uint8, 2 * n, gpu)
+                                    and _fits(ckpt_scales, torch.float32, n // 64, gpu)))):
+        _dev(x)
+        _arg(q, "q", torch.uint8, n // per, x.device)
+        _arg(scales, "scales", sdt, n // block, x.device)
+        _arg(ckpt, "ckpt", torch.uint8, 2 * n, x.device, optional=not checkpoint)
+        _arg(ckpt_scales, "ckpt_scales", torch.float32, n // 64, x.device, optional=not checkpoint)
+    _check("swiglu_quantize", _lib.swiglu_quantize(
+        x.data_ptr(), _dtype_code(dt), rows, ffn, ROWS.get(fmt, 99), q.data_ptr(), scales.data_ptr(),
+        _ptr(ckpt), _ptr(ckpt_scales), _stream_on(gpu, stream)))
+    return q, scales, ckpt, ckpt_scales
+
+
+def swiglu_backward(dy, ckpt, ckpt_scales, fmt=None, dx=None, q=None, scales=None, stream=None):
+    """Gradient of silu(g) * u at the checkpoint's values -> (dx, q, scales).
+
+    fmt None: dx [.., 2 ffn] in dy's dtype, q and scales None.  fmt "mxfp4" or
+    "fp8": dx as quantized rows q, scales of [.., 2 ffn]; dx itself is written
+    too where a tensor for it is given, else None."""
+    if fmt is None and (q is not None or scales is not None):
+        raise ValueError("fmt is required with q and scales")
+    if stream is not None and ((dx is None if fmt is None else q is None or scales is None)):
+        return _on_stream(swiglu_backward, locals())
+    ckpt = _codes(ckpt)
+    shape, gpu, dt = dy.shape, dy.get_device(), dy.dtype
+    ffn, lead = shape[-1], shape[:-1]
+    rows = dy.numel() // ffn if ffn else 0
+    n = rows * ffn
+    fp8 = fmt == "fp8"
+    per, block, sdt = (1, 128, torch.float32) if fp8 else (2, 32, torch.uint8)
+    if fmt is None:
+        if dx is None:
+            dx = dy.new_empty((*lead, 2 * ffn))
+    else:
+        if q is None:
+            q = dy.new_empty((*lead, 2 * ffn // per), dtype=torch.uint8)
+        if scales is None:
+            scales = dy.new_empty((*lead, 2 * ffn // block), dtype=sdt)
+        q = _codes(q)
+    if not (gpu >= 0 and _fits(dy, dt, n, gpu) and _fits(ckpt, torch.uint8, 2 * n, gpu)
+            and _fits(ckpt_scales, torch.float32, n // 64, gpu) and (dx is None or _fits(dx, dt, 2 * n, gpu))
+            and (q is None or (_fits(q, torch.uint8, 2 * n // per, gpu) and _fits(scales, sdt, 2 * n // block, gpu)))):
+        _dev(dy)
+        _arg(ckpt, "ckpt", torch.uint8, 2 * n, dy.device)
+        _arg(ckpt_scales, "ckpt_scales", torch.float32, n // 64, dy.device)
+        _arg(dx, "dx", dt, 2 * n, dy.device, optional=True)
+        _arg(q, "q", torch.uint8, 2 * n // per, dy.device, optional=True)
+        _arg(scales, "scales", sdt, 2 * n // block, dy.device, optional=True)
+    _check("swiglu_backward", _lib.swiglu_backward(
+        dy.data_ptr(), _dtype_code(dt), ckpt.data_ptr(), ckpt_scales.data_ptr(), rows, ffn, _ptr(dx),
+        ROWS.get(fmt, 99), _ptr(q), _ptr(scales), _stream_on(gpu, stream)))
+    return dx, q, scales
+
+
+def _mask_bytes(mask):
+    """A mask of tokens as bytes, whichever dtype it came in."""
+    return mask.view(torch.uint8) if mask is not None and mask.dtype is torch.bool else mask
+
+
+def router_balance(logits, experts, coef=1.0, mask=None, loss=None, counts=None, offsets=None,
+                   prob_grad=None, workspace=None, stream=None):
+    """Balance loss of a router -> (loss fp32 [1], counts int32 [E], offsets
+    int64 [E+1], prob_grad fp32 [E]).
+
+    logits [.., E]; experts int32 or int64 [.., k], the experts that each token
+    goes to (torch.topk's indices); mask, bool or uint8 [..]: tokens that count.
+    loss is coef E / (k n^2) sum_e counts_e sum_t softmax(logits_t)_e; offsets are
+    the grouped products' token_offsets for slots sorted by expert; prob_grad is
+    for router_balance_backward.  workspace: uint8 of at least
+    router_balance_workspace(tokens, E) elements (allocated if None)."""
+    if stream is not None and (loss is None or counts is None or offsets is None or prob_grad is None
+                               or workspace is None):
+        return _on_stream(router_balance, locals())
+    mask = _mask_bytes(mask)
+    gpu, dt, E, k = logits.get_device(), logits.dtype, logits.shape[-1], experts.shape[-1]
+    tokens = logits.numel() // E if E else 0
+    size = 4 if experts.dtype is torch.int32 else 8
+    idt = torch.int32 if size == 4 else torch.int64
+    need = _lib.router_balance_workspace(tokens, E)
+    if loss is None:
+        loss = logits.new_empty(1, dtype=torch.float32)
+    if counts is None:
+        counts = logits.new_empty(E, dtype=torch.int32)
+    if offsets is None:
+        offsets = logits.new_empty(E + 1, dtype=torch.int64)
+    if prob_grad is None:
+        prob_grad = logits.new_empty(E, dtype=torch.float32)
+    if workspace is None:
+        workspace = logits.new_empty(need, dtype=torch.uint8)
+    if not (gpu >= 0 and _fits(logits, dt, tokens * E, gpu) and _fits(experts, idt, tokens * k, gpu)
+            and (mask is None or _fits(mask, torch.uint8, tokens, gpu)) and _fits(loss, torch.float32, 1, gpu)
+            and _fits(counts, torch.int32, E, gpu) and _fits(offsets, torch.int64, E + 1, gpu)
+            and _fits(prob_grad, torch.float32, E, gpu) and _fits(workspace, torch.uint8, need, gpu)):
+        _dev(logits)
+        _arg(experts, "experts", idt, tokens * k, logits.device)
+        _arg(mask, "mask", torch.uint8, tokens, logits.device, optional=True)
+        _arg(loss, "loss", torch.float32, 1, logits.device)
+        _arg(counts, "counts", torch.int32, E, logits.device)
+        _arg(offsets, "offsets", torch.int64, E + 1, logits.device)
+        _arg(prob_grad, "prob_grad", torch.float32, E, logits.device)
+        _arg(workspace, "workspace", torch.uint8, need, logits.device)
+    _check("router_balance", _lib.router_balance(
+        logits.data_ptr(), _dtype_code(dt), experts.data_ptr(), size, _ptr(mask), tokens, E, k, coef,
+        loss.data_ptr(), counts.data_ptr(), offsets.data_ptr(), prob_grad.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _stream_on(gpu, stream)))
+    return loss, counts, offsets, prob_grad
+
+
+def router_balance_workspace(tokens, num_experts):
+    """Bytes of router_balance's workspace."""
+    return _lib.router_balance_workspace(tokens, num_experts)
+
+
+def router_balance_backward(logits, prob_grad, dloss=None, mask=None, add=None, dlogits=None, stream=None):
+    """Gradient of the balance loss -> dlogits in logits' dtype and shape.
+
+    prob_grad as router_balance returned it; dloss: fp32 [1] on the GPU, the
+    loss' own gradient (1 if None); add: the gradient that reaches the logits
+    otherwise.  dlogits may be add or logits itself."""
+    if stream is not None and dlogits is None:
+        return _on_stream(router_balance_backward, locals())
+    mask = _mask_bytes(mask)
+    gpu, dt, n, E = logits.get_device(), logits.dtype, logits.numel(), logits.shape[-1]
+    tokens = n // E if E else 0
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    if not (gpu >= 0 and _fits(logits, dt, n, gpu) and _fits(prob_grad, torch.float32, E, gpu)
+            and (dloss is None or _fits(dloss, torch.float32, 1, gpu))
+            and (mask is None or _fits(mask, torch.uint8, tokens, gpu))
+            and (add is None or _fits(add, dt, n, gpu)) and _fits(dlogits, dt, n, gpu)):
+        _dev(logits)
+        _arg(prob_grad, "prob_grad", torch.float32, E, logits.device)
+        _arg(dloss, "dloss", torch.float32, 1, logits.device, optional=True)
+        _arg(mask, "mask", torch.uint8, tokens, logits.device, optional=True)
+        _arg(add, "add", dt, n, logits.device, optional=True)
+        _arg(dlogits, "dlogits", dt, n, logits.device)
+    _check("router_balance_backward", _lib.router_balance_backward(
+        logits.data_ptr(), _dtype_code(dt), prob_grad.data_ptr(), _ptr(dloss), _ptr(mask), _ptr(add),
+        tokens, E, dlogits.data_ptr(), _stream_on(gpu, stream)))
+    return dlogits
 
 
 class ErrorFeedback:

@@ -11,7 +11,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp4mi.so")
-SOURCES = ["quant.hip", "fp4quant.hip", "fp8col.hip", "matmul.hip", "wgrad.hip", "rmsnorm.hip", "abi.hip"]
+SOURCES = ["quant.hip", "fp4quant.hip", "fp8col.hip", "matmul.hip", "wgrad.hip", "rmsnorm.hip",
+           "fp8quant.hip", "fp8mat.hip", "swiglu.hip", "router.hip", "abi.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

@@ -17,27 +17,6 @@ namespace {
 // flight at once; splitting k inside the workgroup needs no second launch.  What
 // bounds it is the number of vector loads, then memory: 4096 x 7168 by one token
 // 4.8 us, 64 tokens over 32 experts of 2048 x 7168 29.1 us (4.8 TB/s).
-template <bool A8>
-struct LaneStep {   // one lane's part of one 16-row operand at one step
-  Frag<A8> v;
-  int s;
-};
-
-// Row `row` of an operand at step `st`, group g.
-template <bool A8>
-__device__ __forceinline__ void load_lane(const uint8_t* base, const void* scales, int64_t row,
-                                          int k, int st, int g, LaneStep<A8>& o) {
-  const int at = st * 128 + 32 * g;
-  if constexpr (A8) {
-    const i32x4* p = reinterpret_cast<const i32x4*>(base + row * k + at);
-    o.v.lo = p[0];
-    o.v.hi = p[1];
-    o.s = (int)e8m0_of(static_cast<const float*>(scales)[row * (k >> 7) + st]);
-  } else {
-    o.v.lo = *reinterpret_cast<const i32x4*>(base + row * (k >> 1) + (at >> 1));
-    o.s = static_cast<const uint8_t*>(scales)[row * (k >> 5) + (at >> 5)];
-  }
-}
 
 // 4 scale bytes of a row of `bytes` >= 4 from byte `at`.  Past the row's end
 // stand other bytes of the row: the codes there count as zero, and a NaN scale
@@ -204,32 +183,10 @@ void launch_rows(ProductArgs p, int out_dtype, hipStream_t st) {
 // at the 1.8 GHz that the card holds under this load; each of a compute unit's 4
 // tiles has 10 us of start and output around it, and with the LDS reads, direct
 // loads and scales left out the rest takes 183 us in place of 255.
-typedef __amdgpu_buffer_rsrc_t buffer_t;
-__device__ __forceinline__ buffer_t buffer_of(const void* base, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
-}
-// 16 bytes a lane from base + v + s to l + 16 lane; l is the wave's.
-__device__ __forceinline__ void load_to_lds(buffer_t b, uint32_t v, uint32_t s, void* l) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)l, 16, (int)v,
-                                           (int)s, 0, 0);
-}
-
 template <int SA, int SB>
 __device__ __forceinline__ f32x16 mfma_scaled32(i32x4 a, i32x4 b, f32x16 c, int sa, int sb) {
   const i32x8 x = {a.x, a.y, a.z, a.w, 0, 0, 0, 0}, y = {b.x, b.y, b.z, b.w, 0, 0, 0, 0};
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, kE2M1, kE2M1, SA, sa, SB, sb);
-}
-
-// Byte j of four words -> word j.
-__device__ __forceinline__ void transpose_bytes(const uint32_t (&w)[4], uint32_t (&t)[4]) {
-  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u);
-  const uint32_t b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
-  const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
-  const uint32_t d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
-  t[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
-  t[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
-  t[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
-  t[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
 }
 
 template <int FN, int FM>

@@ -19,7 +19,6 @@ namespace fp4mi {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kE2M1 = 4;   // the instruction's operand format field
@@ -168,6 +167,39 @@ __device__ __forceinline__ void mfma_bf16_step(const LA (&a)[N], const LB (&b)[M
 // byte 0); sign and fraction bits are not read.
 __device__ __forceinline__ uint32_t e8m0_of(float s) {
   return (__float_as_uint(s) >> 23) & 0xFFu;
+}
+
+template <bool A8>
+struct LaneStep {   // one lane's part of one 16-row operand at one step
+  Frag<A8> v;
+  int s;
+};
+
+// Row `row` of an operand at step `st`, group g.
+template <bool A8>
+__device__ __forceinline__ void load_lane(const uint8_t* base, const void* scales, int64_t row,
+                                          int k, int st, int g, LaneStep<A8>& o) {
+  const int at = st * 128 + 32 * g;
+  if constexpr (A8) {
+    const i32x4* p = reinterpret_cast<const i32x4*>(base + row * k + at);
+    o.v.lo = p[0];
+    o.v.hi = p[1];
+    o.s = (int)e8m0_of(static_cast<const float*>(scales)[row * (k >> 7) + st]);
+  } else {
+    o.v.lo = *reinterpret_cast<const i32x4*>(base + row * (k >> 1) + (at >> 1));
+    o.s = static_cast<const uint8_t*>(scales)[row * (k >> 5) + (at >> 5)];
+  }
+}
+
+// ------------------------------------------------------ direct loads to LDS
+typedef __amdgpu_buffer_rsrc_t buffer_t;
+__device__ __forceinline__ buffer_t buffer_of(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
+}
+// 16 bytes a lane from base + v + s to l + 16 lane; l is the wave's.
+__device__ __forceinline__ void load_to_lds(buffer_t b, uint32_t v, uint32_t s, void* l) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)l, 16, (int)v,
+                                           (int)s, 0, 0);
 }
 
 // Operands of C[t, :] = A[t, :] . W[e]^T, rows t of shard e.  offsets is

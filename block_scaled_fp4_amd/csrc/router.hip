@@ -1,0 +1,420 @@
+// The router's balance loss, the tokens of each expert, and the loss' gradient.
+#include <math.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "fp4mi_moe.h"
+#include "host_common.hpp"
+#include "rows_common.hpp"
+
+namespace fp4mi {
+namespace {
+
+constexpr int kMaxExperts = 4096;
+
+// Four elements from element i, at any alignment of their type.
+template <bool BF16>
+__device__ __forceinline__ f32x4 load4(const void* base, int64_t i) {
+  if constexpr (BF16) {
+    u32x2 w;
+    memcpy(&w, static_cast<const uint16_t*>(base) + i, 8);
+    return f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+  } else {
+    f32x4 v;
+    memcpy(&v, static_cast<const float*>(base) + i, 16);
+    return v;
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ float load1(const void* base, int64_t i) {
+  if constexpr (BF16) return bf16_lo(static_cast<const uint16_t*>(base)[i]);
+  else return static_cast<const float*>(base)[i];
+}
+template <bool BF16>
+__device__ __forceinline__ void store4(void* base, int64_t i, f32x4 v) {
+  if constexpr (BF16) {
+    const u32x2 w = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+    memcpy(static_cast<uint16_t*>(base) + i, &w, 8);
+  } else {
+    memcpy(static_cast<float*>(base) + i, &v, 16);
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void store1(void* base, int64_t i, float v) {
+  if constexpr (BF16) static_cast<uint16_t*>(base)[i] = (uint16_t)pack_bf16x2(v, v);
+  else static_cast<float*>(base)[i] = v;
+}
+
+// A row of E values over L lanes, 4 CH of them a lane: chunk c of lane l holds
+// columns 4 (c L + l) .. + 3, `fill` past the row's end.
+template <bool BF16, int L, int CH>
+__device__ __forceinline__ void load_row(const void* base, int64_t row, int experts, int l, float fill,
+                                         f32x4 (&v)[CH]) {
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int e = 4 * (c * L + l);
+    if (e + 4 <= experts) {
+      v[c] = load4<BF16>(base, row * experts + e);
+    } else {
+      v[c] = f32x4{fill, fill, fill, fill};
+      for (int j = 0; j < 3; ++j)
+        if (e + j < experts) v[c][j] = load1<BF16>(base, row * experts + e + j);
+    }
+  }
+}
+
+template <int L, typename F>
+__device__ __forceinline__ float over_lanes(float v, F f) {
+#pragma unroll
+  for (int d = 1; d < L; d <<= 1) v = f(v, __shfl_xor(v, d));
+  return v;
+}
+
+// The softmax of a row in place.  A row of -inf alone becomes zeros; NaN and
+// +inf make the row NaN.
+template <int L, int CH>
+__device__ __forceinline__ void softmax_row(f32x4 (&v)[CH]) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) top = fmaxf(fmaxf(fmaxf(v[c].x, v[c].y), fmaxf(v[c].z, v[c].w)), top);
+  top = over_lanes<L>(top, [](float a, float b) { return fmaxf(a, b); });
+  if (top == -INFINITY) top = 0.0f;
+  float sum = 0.0f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[c][j] = exp_f32(v[c][j] - top);
+      sum += v[c][j];
+    }
+  }
+  sum = over_lanes<L>(sum, [](float a, float b) { return a + b; });
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) v[c] *= inv;
+}
+
+struct BalanceArgs {
+  const void* x;
+  const void* idx;
+  const uint8_t* mask;
+  int64_t tokens;
+  int64_t slots;       // tokens * k
+  int experts, k;
+  float coef;
+  float* loss;
+  int32_t* counts;
+  int64_t* offsets;
+  float* grad;
+  float* part_p;       // [blocks, E]
+  int32_t* part_c;     // [blocks, E]
+  int32_t* part_n;     // [blocks]
+  int blocks;
+};
+
+// A workgroup adds its rows' p in registers, row after row, its waves' sums in
+// LDS in the order of the waves, and leaves them, its counts and its number of
+// counted tokens in the workspace.
+template <bool BF16, bool IDX64, int L, int CH, int W>
+__global__ __launch_bounds__(64 * W) void balance_kernel(BalanceArgs p) {
+  constexpr int R = 64 / L;   // rows a wave takes at once
+  __shared__ float sums[L * CH * 4];
+  __shared__ int hist[L * CH * 4];
+  __shared__ int counted[W];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (L - 1), sub = lane / L;
+  for (int e = tid; e < L * CH * 4; e += 64 * W) {
+    sums[e] = 0.0f;
+    hist[e] = 0;
+  }
+  __syncthreads();
+  f32x4 acc[CH] = {}, cur[CH], next[CH];
+  int n = 0;
+  const int64_t step = (int64_t)p.blocks * W * R;
+  int64_t row = ((int64_t)blockIdx.x * W + wave) * R + sub;
+  if (row < p.tokens) load_row<BF16, L, CH>(p.x, row, p.experts, l, -INFINITY, next);
+  for (; row < p.tokens; row += step) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) cur[c] = next[c];
+    const bool in = !p.mask || p.mask[row];
+    if (row + step < p.tokens) load_row<BF16, L, CH>(p.x, row + step, p.experts, l, -INFINITY, next);
+    softmax_row<L, CH>(cur);
+    if (in) {   // not p times 0: a row that is not counted may hold anything
+      ++n;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) acc[c] += cur[c];
+    }
+  }
+  for (int64_t s = (int64_t)blockIdx.x * (64 * W) + tid; s < p.slots; s += (int64_t)p.blocks * (64 * W)) {
+    const uint64_t e = IDX64 ? (uint64_t)static_cast<const int64_t*>(p.idx)[s]
+                             : (uint64_t)(int64_t)static_cast<const int32_t*>(p.idx)[s];
+    if (e < (uint64_t)p.experts && (!p.mask || p.mask[(uint32_t)s / (uint32_t)p.k])) atomicAdd(&hist[e], 1);
+  }
+#pragma unroll
+  for (int d = L; d < 64; d <<= 1) {   // rows of a wave
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[c][j] += __shfl_xor(acc[c][j], d);
+    n += __shfl_xor(n, d);
+  }
+  if (lane == 0) counted[wave] = n;
+  for (int w = 0; w < W; ++w) {
+    if (wave == w && sub == 0) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sums[4 * (c * L + l) + j] += acc[c][j];
+    }
+    __syncthreads();
+  }
+  for (int e = tid; e < p.experts; e += 64 * W) {
+    p.part_p[(int64_t)blockIdx.x * p.experts + e] = sums[e];
+    p.part_c[(int64_t)blockIdx.x * p.experts + e] = hist[e];
+  }
+  if (tid == 0) {
+    int total = 0;
+    for (int w = 0; w < W; ++w) total += counted[w];
+    p.part_n[blockIdx.x] = total;
+  }
+}
+
+// Adds the workgroups' parts, in fp64 and in a fixed order, and writes what
+// follows from them.  One workgroup: Q groups of threads take every Q-th part.
+__global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs p) {
+  __shared__ double dsum[1024];
+  __shared__ int isum[1024];
+  __shared__ int count[kMaxExperts];
+  const int tid = threadIdx.x;
+  int width = 1024;   // threads across the experts
+  while (width / 2 >= p.experts && width > 64) width /= 2;
+  const int q = tid / width, Q = 1024 / width;
+  int n = 0;
+  for (int b = tid; b < p.blocks; b += 1024) n += p.part_n[b];
+  isum[tid] = n;
+  __syncthreads();
+  for (int d = 512; d; d >>= 1) {
+    if (tid < d) isum[tid] += isum[tid + d];
+    __syncthreads();
+  }
+  const double tokens = (double)isum[0];
+  __syncthreads();
+  const double share = tokens > 0.0 ? (double)p.coef * p.experts / ((double)p.k * tokens * tokens) : 0.0;
+  double loss = 0.0;
+  for (int e0 = 0; e0 < p.experts; e0 += width) {   // one round where Q > 1
+    const int e = e0 + tid % width;
+    double s = 0.0;
+    int c = 0;
+    if (e < p.experts) {
+      for (int b = q; b < p.blocks; b += Q) {
+        s += (double)p.part_p[(int64_t)b * p.experts + e];
+        c += p.part_c[(int64_t)b * p.experts + e];
+      }
+    }
+    dsum[tid] = s;
+    isum[tid] = c;
+    __syncthreads();
+    if (q == 0 && e < p.experts) {
+      for (int o = 1; o < Q; ++o) {
+        s += dsum[tid + o * width];
+        c += isum[tid + o * width];
+      }
+      count[e] = c;
+      p.counts[e] = c;
+      p.grad[e] = (float)(share * c);
+      if (tokens > 0.0) loss += share * c * s;
+    }
+  }
+  __syncthreads();
+  dsum[tid] = loss;
+  __syncthreads();
+  for (int d = 512; d; d >>= 1) {
+    if (tid < d) dsum[tid] += dsum[tid + d];
+    __syncthreads();
+  }
+  if (tid == 0) *p.loss = (float)dsum[0];
+  if (tid < 64) {   // sums of the counts before each expert
+    int64_t base = 0;
+    for (int e0 = 0; e0 < p.experts; e0 += 64) {
+      const int c = e0 + tid < p.experts ? count[e0 + tid] : 0;
+      int sum = c;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(sum, d);
+        if (tid >= d) sum += v;
+      }
+      if (e0 + tid < p.experts) p.offsets[e0 + tid] = base + sum - c;
+      base += __builtin_amdgcn_readlane(sum, 63);
+    }
+    if (tid == 0) p.offsets[p.experts] = base;
+  }
+}
+
+struct BalanceGradArgs {
+  const void* x;
+  const float* v;
+  const float* dloss;
+  const uint8_t* mask;
+  const void* add;
+  void* out;
+  int64_t tokens;
+  int experts;
+  int blocks;
+};
+
+template <bool BF16, int L, int CH, int W>
+__global__ __launch_bounds__(64 * W) void balance_grad_kernel(BalanceGradArgs p) {
+  constexpr int R = 64 / L;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (L - 1), sub = lane / L;
+  f32x4 v[CH], cur[CH], next[CH];
+  load_row<false, L, CH>(p.v, 0, p.experts, l, 0.0f, v);
+  const float dl = p.dloss ? *p.dloss : 1.0f;
+  const int64_t step = (int64_t)p.blocks * W * R;
+  int64_t row = ((int64_t)blockIdx.x * W + wave) * R + sub;
+  if (row < p.tokens) load_row<BF16, L, CH>(p.x, row, p.experts, l, -INFINITY, next);
+  for (; row < p.tokens; row += step) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) cur[c] = next[c];
+    const bool in = !p.mask || p.mask[row];
+    f32x4 add[CH] = {};
+    if (p.add) load_row<BF16, L, CH>(p.add, row, p.experts, l, 0.0f, add);
+    if (row + step < p.tokens) load_row<BF16, L, CH>(p.x, row + step, p.experts, l, -INFINITY, next);
+    softmax_row<L, CH>(cur);
+    float dot = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dot = fmaf(cur[c][j], v[c][j], dot);
+    dot = over_lanes<L>(dot, [](float a, float b) { return a + b; });
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int e = 4 * (c * L + l);
+      f32x4 d = add[c];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (in) d[j] += dl * cur[c][j] * (v[c][j] - dot);
+      if (e + 4 <= p.experts) {
+        store4<BF16>(p.out, row * p.experts + e, d);
+      } else {
+        for (int j = 0; j < 3; ++j)
+          if (e + j < p.experts) store1<BF16>(p.out, row * p.experts + e + j, d[j]);
+      }
+    }
+  }
+}
+
+// Lanes of a row and its chunks a lane: the fewest lanes that hold it in one
+// chunk, then more chunks.  f(integral constants L, CH, W).
+template <int N>
+using Int = std::integral_constant<int, N>;
+template <typename F>
+void by_width(int experts, F f) {
+  if (experts <= 32) f(Int<8>(), Int<1>(), Int<16>());
+  else if (experts <= 64) f(Int<16>(), Int<1>(), Int<16>());
+  else if (experts <= 128) f(Int<32>(), Int<1>(), Int<16>());
+  else if (experts <= 256) f(Int<64>(), Int<1>(), Int<16>());
+  else if (experts <= 512) f(Int<64>(), Int<2>(), Int<16>());
+  else if (experts <= 1024) f(Int<64>(), Int<4>(), Int<8>());
+  else f(Int<64>(), Int<16>(), Int<4>());
+}
+
+constexpr int kBalanceBlocks = 256;
+int balance_blocks(int64_t tokens, int experts) {
+  int64_t blocks = 0;
+  by_width(experts, [&](auto l, auto, auto w) {
+    constexpr int rows = 64 / decltype(l)::value * decltype(w)::value;
+    blocks = (tokens + rows - 1) / rows;
+  });
+  return (int)(blocks < 1 ? 1 : (blocks < kBalanceBlocks ? blocks : kBalanceBlocks));
+}
+
+}  // namespace
+}  // namespace fp4mi
+
+using namespace fp4mi;
+
+extern "C" int64_t router_balance_workspace(int64_t tokens, int32_t num_experts) {
+  if (tokens < 0 || tokens >= (int64_t(1) << 31) || num_experts < 1 || num_experts > kMaxExperts) return 0;
+  return (int64_t)balance_blocks(tokens, num_experts) * (8 * num_experts + 4);
+}
+
+extern "C" int router_balance(const void* logits, int dtype, const void* experts, int index_size,
+                              const uint8_t* mask, int64_t tokens, int32_t num_experts, int32_t k,
+                              float coef, float* loss, int32_t* counts, int64_t* offsets,
+                              float* prob_grad, void* workspace, int64_t workspace_bytes,
+                              void* stream) {
+  const int isz = dtype_size(dtype);
+  if (!isz) return FP4_EDTYPE;
+  if ((index_size != 4 && index_size != 8) || !(fabsf(coef) < INFINITY)) return FP4_EINVAL;
+  if (tokens < 0 || tokens >= (int64_t(1) << 31) || num_experts < 1 || num_experts > kMaxExperts ||
+      k < 1 || (tokens && k > ((int64_t(1) << 31) - 1) / tokens))
+    return FP4_ESHAPE;
+  const int64_t need = router_balance_workspace(tokens, num_experts), slots = tokens * k;
+  if (workspace_bytes < need) return FP4_ESHAPE;
+  if ((tokens && (!logits || !experts)) || !loss || !counts || !offsets || !prob_grad || !workspace)
+    return FP4_EINVAL;
+  if (!is_aligned(logits, isz) || !is_aligned(experts, index_size) || !is_aligned(loss, 4) ||
+      !is_aligned(counts, 4) || !is_aligned(offsets, 8) || !is_aligned(prob_grad, 4) ||
+      !is_aligned(workspace, 16))
+    return FP4_EALIGN;
+  const void* outs[5] = {loss, counts, offsets, prob_grad, workspace};
+  const int64_t outn[5] = {4, 4 * (int64_t)num_experts, 8 * ((int64_t)num_experts + 1),
+                           4 * (int64_t)num_experts, need};
+  const void* ins[3] = {logits, experts, mask};
+  const int64_t inn[3] = {tokens * num_experts * isz, slots * index_size, tokens};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 3; ++j)
+      if (overlaps(outs[i], outn[i], ins[j], inn[j])) return FP4_EOVERLAP;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i], outn[i], outs[j], outn[j])) return FP4_EOVERLAP;
+  }
+  BalanceArgs p = {logits, experts, mask, tokens, slots, num_experts, k, coef, loss, counts, offsets, prob_grad};
+  p.blocks = balance_blocks(tokens, num_experts);
+  p.part_p = static_cast<float*>(workspace);
+  p.part_c = reinterpret_cast<int32_t*>(p.part_p + (int64_t)p.blocks * num_experts);
+  p.part_n = p.part_c + (int64_t)p.blocks * num_experts;
+  clear_stale_error();
+  hipStream_t st = as_stream(stream);
+  const bool bf16 = dtype == FP4_DTYPE_BF16, wide = index_size == 8;
+  by_width(num_experts, [&](auto l, auto ch, auto w) {
+    constexpr int L = decltype(l)::value, CH = decltype(ch)::value, W = decltype(w)::value;
+    hipLaunchKernelGGL((bf16 ? (wide ? balance_kernel<true, true, L, CH, W> : balance_kernel<true, false, L, CH, W>)
+                             : (wide ? balance_kernel<false, true, L, CH, W> : balance_kernel<false, false, L, CH, W>)),
+                       dim3(p.blocks), dim3(64 * W), 0, st, p);
+  });
+  hipLaunchKernelGGL(balance_join_kernel, dim3(1), dim3(1024), 0, st, p);
+  return launch_status();
+}
+
+extern "C" int router_balance_backward(const void* logits, int dtype, const float* prob_grad,
+                                       const float* dloss, const uint8_t* mask, const void* add,
+                                       int64_t tokens, int32_t num_experts, void* dlogits,
+                                       void* stream) {
+  const int isz = dtype_size(dtype);
+  if (!isz) return FP4_EDTYPE;
+  if (tokens < 0 || tokens >= (int64_t(1) << 31) || num_experts < 1 || num_experts > kMaxExperts)
+    return FP4_ESHAPE;
+  if (tokens == 0) return FP4_OK;
+  if (!logits || !prob_grad || !dlogits) return FP4_EINVAL;
+  if (!is_aligned(logits, isz) || !is_aligned(prob_grad, 4) || !is_aligned(dloss, 4) ||
+      !is_aligned(add, isz) || !is_aligned(dlogits, isz))
+    return FP4_EALIGN;
+  const int64_t n = tokens * num_experts * isz;
+  if ((dlogits != logits && overlaps(dlogits, n, logits, n)) ||
+      (dlogits != add && overlaps(dlogits, n, add, n)) ||
+      overlaps(dlogits, n, prob_grad, 4 * (int64_t)num_experts) || overlaps(dlogits, n, dloss, 4) ||
+      overlaps(dlogits, n, mask, tokens))
+    return FP4_EOVERLAP;
+  BalanceGradArgs p = {logits, prob_grad, dloss, mask, add, dlogits, tokens, num_experts, 0};
+  clear_stale_error();
+  hipStream_t st = as_stream(stream);
+  by_width(num_experts, [&](auto l, auto ch, auto) {
+    constexpr int L = decltype(l)::value, CH = decltype(ch)::value, W = 4, rows = 64 / L * W;
+    const int64_t blocks = (tokens + rows - 1) / rows;
+    p.blocks = (int)(blocks < 2048 ? blocks : 2048);
+    hipLaunchKernelGGL((dtype == FP4_DTYPE_BF16 ? balance_grad_kernel<true, L, CH, W>
+                                                : balance_grad_kernel<false, L, CH, W>),
+                       dim3(p.blocks), dim3(64 * W), 0, st, p);
+  });
+  return launch_status();
+}

@@ -287,6 +287,203 @@ void launch_exact_tiles(Fp8Args p, int out_dtype, hipStream_t st) {
     launch_1d(fp8_exact_tiles_kernel<WM, false>, blocks, 128 * WM, st, p);
 }
 
+// ------------------------------------------------ many rows, bf16 outputs
+// One workgroup of four waves owns 256 columns of W by 64 FM tokens, each wave 128
+// by 32 FM in 32 x 32 x 64 scaled instructions (lane l: row l % 32, the 32 k of
+// group l / 32; D's lane l: column l % 32, rows 8 (i / 4) + 4 (l / 32) + i % 4).
+// k runs in halves of a scale block, 64 bytes of every row, through a ring of four
+// buffers in LDS: while half h is multiplied from registers, the fragments of h + 1
+// are read, h + 2 and h + 3 are on their way and h + 4 is asked for, into the
+// buffer that h left.  A row's four 16-byte chunks lie at position chunk ^ (row / 4
+// % 4): 16 rows of a fragment read then take every bank once.
+template <int FM>
+struct Fp8TileShared {
+  uint8_t w[4][256 * 64];
+  uint8_t x[4][64 * FM * 64];
+  // scales of eight stages of 128 k: bytes of rows r, r + 32, .. of a wave's half
+  uint32_t ws[8][2][32], xs[8][2][32];
+};
+
+template <int SA, int SB>
+__device__ __forceinline__ f32x16 mfma_fp8(const Frag<true>& a, const Frag<true>& b, f32x16 c, int sa, int sb) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(words(a), words(b), c, kE4M3, kE4M3, SA, sa, SB, sb);
+}
+
+template <int FM>
+__global__ __launch_bounds__(256, 1) void fp8_tiles_kernel(Fp8Args p, int64_t blk0) {
+  constexpr int FN = 4, BM = 64 * FM, kAll = FN * FM, kLoads = FN + FM;
+  __shared__ __align__(16) union {
+    Fp8TileShared<FM> t;
+    uint8_t out[4][quarter_bytes<FN, true>()];
+  } sh;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t blk = (int64_t)blockIdx.x + blk0;
+  const int nt = (int)(blk % p.n_tiles), mt = (int)(blk / p.n_tiles);
+  int e = 0, row0 = p.offsets ? 0 : mt * BM, row_end = (int)p.tokens;
+  if (p.offsets) {
+    if (!locate_tile<BM>(p.offsets, p.experts, (int)p.tokens, mt, e, row0, row_end)) return;
+  }
+  const int n0 = nt * 256, stages = p.k >> 7, halves = 2 * stages;
+  const int wrows = p.n - n0, xrows = row_end - row0;
+  const uint8_t* w = p.w + ((int64_t)e * p.n + n0) * p.k;
+  const uint8_t* x = p.a + (int64_t)row0 * p.k;
+  const int wn = wave & 1, wm = wave >> 1;   // this wave's quarter
+
+  // Direct loads: an instruction covers 16 rows; lane l is row l / 4, position l % 4.
+  const int ch = (lane & 3) ^ (lane >> 4);
+  uint32_t wo[FN], xo[FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+    wo[i] = (uint32_t)min(16 * (wave * FN + i) + (lane >> 2), wrows - 1) * (uint32_t)p.k + ch * 16;
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+    xo[i] = (uint32_t)min(16 * (wave * FM + i) + (lane >> 2), xrows - 1) * (uint32_t)p.k + ch * 16;
+  const buffer_t wb = buffer_of(w, (int64_t)min(wrows, 256) * p.k);
+  const buffer_t xb = buffer_of(x, (int64_t)min(xrows, BM) * p.k);
+  auto fetch = [&](auto b, int h, int i) {   // past the end the last half again, which nobody reads
+    constexpr int B = decltype(b)::value & 3;
+    const uint32_t so = (uint32_t)min(h, halves - 1) * 64;
+    if (i < FN) load_to_lds(wb, wo[i < FN ? i : 0], so, &sh.t.w[B][(wave * FN + i) * 1024]);
+    else load_to_lds(xb, xo[i < FN ? 0 : i - FN], so, &sh.t.x[B][(wave * FM + i - FN) * 1024]);
+  };
+  // Scales, four stages at a time: thread t those of row t of either operand.
+  const float* ws = p.w_scales + ((int64_t)e * p.scale_rows + ((n0 + min(tid, wrows - 1)) >> p.scale_shift)) * stages;
+  const float* xs = p.a_scales + (int64_t)(row0 + min(tid % BM, xrows - 1)) * stages;
+  u32x4 wq, xq;
+  auto fetch_scales = [&](int s) {   // of four stages or more, the last four where s + 3 is past the end
+    const int at = min(s, stages - 4);
+    memcpy(&wq, ws + at, 16);
+    memcpy(&xq, xs + at, 16);
+  };
+  auto put_scales = [&](int s) {
+    const int past = min(max(s - max(stages - 4, 0), 0), 3);   // stages past the end get any scale
+    const auto pack = [&](u32x4& v) {
+      asm volatile("" : "+v"(v));   // else each is loaded as its upper half alone
+      const uint32_t lo = (v[0] >> 23 & 0xFFu) | (v[1] >> 15 & 0xFF00u);
+      const uint32_t all = lo | (v[2] >> 7 & 0xFF0000u) | (v[3] << 1 & 0xFF000000u);
+      return all >> (8 * past);
+    };
+    const uint32_t wb4 = pack(wq), xb4 = pack(xq);
+    const int wat = (tid >> 7) * 128 + (tid & 31) * 4 + ((tid >> 5) & 3);
+    const int xat = tid % BM / (32 * FM) * 128 + (tid & 31) * 4 + (tid >> 5) % FM;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      reinterpret_cast<uint8_t*>(sh.t.ws)[((s + j) & 7) * 256 + wat] = (uint8_t)(wb4 >> (8 * j));
+      reinterpret_cast<uint8_t*>(sh.t.xs)[((s + j) & 7) * 256 + xat] = (uint8_t)(xb4 >> (8 * j));
+    }
+  };
+
+  const int r = lane & 31, g = lane >> 5;
+  struct Step {
+    Frag<true> w[FN], x[FM];
+  };
+  Step step[2];
+  int wsc, xsc, wsn, xsn;   // scale words of this stage and the next
+  const int c0 = ((2 * g) ^ ((r >> 2) & 3)) * 16;
+  const uint8_t *wl = &sh.t.w[0][(wn * 128 + r) * 64], *xl = &sh.t.x[0][(wm * 32 * FM + r) * 64];
+  // Piece i of the fragments of a half in buffer B: both chunks of fragment i / 2.
+  auto read = [&](auto b, int i, Step& o) {
+    constexpr int B = decltype(b)::value & 3;
+    const int f = i >> 1, c = (i & 1) ? c0 ^ 16 : c0;
+    i32x4& to = f < FN ? ((i & 1) ? o.w[f < FN ? f : 0].hi : o.w[f < FN ? f : 0].lo)
+                       : ((i & 1) ? o.x[f < FN ? 0 : f - FN].hi : o.x[f < FN ? 0 : f - FN].lo);
+    to = f < FN ? *reinterpret_cast<const i32x4*>(wl + B * 256 * 64 + f * 32 * 64 + c)
+                : *reinterpret_cast<const i32x4*>(xl + B * BM * 64 + (f - FN) * 32 * 64 + c);
+  };
+  auto read_scales = [&](int s) {
+    wsn = (int)sh.t.ws[s & 7][wn][r];
+    xsn = (int)sh.t.xs[s & 7][wm][r];
+  };
+  f32x16 acc[FN][FM] = {};
+
+  constexpr int kPieces = 2 * kLoads, kPer = 2 * kPieces / kAll;   // read behind the first half of the products
+  constexpr int kWait = kAll == 16 ? 11 : 6;                       // the product behind which the waves meet
+  // Half h, in buffer h % 4 (Q, its place among eight, tells); SCALES: its share of
+  // bringing the next four stages' scales.
+  auto half = [&](auto q, auto scales, int h) {
+    constexpr int Q = decltype(q)::value, B = Q & 3;
+    const Step& cur = step[B & 1];
+    Step& next = step[(B + 1) & 1];
+    if ((B & 1) == 0) {
+      wsc = wsn;
+      xsc = xsn;
+    }
+    unrolled<kAll>([&](auto idx) {
+      constexpr int i = decltype(idx)::value, I = i / FM, J = i % FM;
+      acc[I][J] = mfma_fp8<I, J>(cur.w[I], cur.x[J], acc[I][J], wsc, xsc);
+      if constexpr (i * kPer < kPieces) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (i * kPer + j < kPieces) read(std::integral_constant<int, (B + 1) & 3>(), i * kPer + j, next);
+      }
+      if constexpr (i < kLoads) fetch(q, h + 4, i);
+      if constexpr (i == kLoads) {
+        if constexpr ((B & 1) == 1) read_scales((h + 1) >> 1);
+        if constexpr (decltype(scales)::value && Q == 0) fetch_scales((h >> 1) + 4);
+        if constexpr (decltype(scales)::value && Q == 4) put_scales((h >> 1) + 2);
+      }
+      if constexpr (i == kWait) {
+        // h + 1 is read, and of this wave's loads all but the last two halves' have landed
+        static_assert(kLoads == 8 || kLoads == 6, "vmcnt");
+        __builtin_amdgcn_s_waitcnt(kLoads == 8 ? 0x4070 : 0x007C);   // lgkmcnt(0), vmcnt(2 kLoads)
+        __builtin_amdgcn_s_barrier();
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    // the sums are made here: left to itself the compiler moves the products past
+    // every branch that follows, to the end of the loop
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) asm volatile("" : "+a"(acc[i][j]));
+  };
+
+  constexpr std::integral_constant<int, 0> b0{};
+  constexpr std::integral_constant<int, 1> b1{};
+  constexpr std::integral_constant<int, 2> b2{};
+  constexpr std::integral_constant<int, 3> b3{};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    wq[j] = __float_as_uint(ws[min(j, stages - 1)]);
+    xq[j] = __float_as_uint(xs[min(j, stages - 1)]);
+  }
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) fetch(b0, 0, i);
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) fetch(b1, 1, i);
+  put_scales(0);
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) fetch(b2, 2, i);
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) fetch(b3, 3, i);
+  __builtin_amdgcn_s_waitcnt(kLoads == 8 ? 0x4070 : 0x007C);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) read(b0, i, step[0]);
+  read_scales(0);
+  __syncthreads();   // all have read half 0: its buffer is free
+  int h = 0;
+  for (; h + 8 <= halves; h += 8) unrolled<8>([&](auto q) { half(q, std::true_type(), h + decltype(q)::value); });
+  for (; h < halves; h += 4) {
+    half(b0, std::false_type(), h);
+    half(b1, std::false_type(), h + 1);
+    if (h + 2 >= halves) break;
+    half(b2, std::false_type(), h + 2);
+    half(b3, std::false_type(), h + 3);
+  }
+  __builtin_amdgcn_s_waitcnt(0x0070);   // what was asked for past the end has landed too
+  __syncthreads();
+  store_quarter<FN, FM, true>(acc, sh.out[wave], p.out, row0 + wm * 32 * FM, row_end, p.n, n0 + wn * 128,
+                              p.a_row_scale);
+}
+
+template <int FM>
+void launch_tiles(Fp8Args p, hipStream_t st) {
+  p.n_tiles = (p.n + 255) / 256;
+  const int64_t blocks = p.n_tiles * max_row_tiles(p.tokens, p.experts, 64 * FM, p.offsets != nullptr);
+  launch_1d(fp8_tiles_kernel<FM>, blocks, 256, st, p);
+}
+
 void launch_product(const Fp8Args& p, int out_dtype, hipStream_t st) {
   const int64_t per = p.tokens / p.experts;
   const bool grouped = p.offsets != nullptr;
@@ -295,6 +492,10 @@ void launch_product(const Fp8Args& p, int out_dtype, hipStream_t st) {
   if (!tiles) {
     if (p.tokens <= 16) launch_rows<1, 1, 8, 4>(p, out_dtype, st);
     else launch_rows<2, 2, 8, 2>(p, out_dtype, st);
+  } else if (out_dtype == FP4_DTYPE_BF16) {
+    const int64_t wide = (int64_t)((p.n + 255) / 256) * max_row_tiles(p.tokens, p.experts, 128, grouped);
+    if (wide > 256 && (!grouped || per >= 256)) launch_tiles<4>(p, st);
+    else launch_tiles<2>(p, st);
   } else {
     launch_exact_tiles<2>(p, out_dtype, st);
   }

@@ -24,7 +24,66 @@ struct Fp8Args {
   int scale_shift;           // row n's scales are row n >> scale_shift of w_scales
   int scale_rows;
   int n_tiles;               // tiles along N
+  int64_t m_tiles;           // row tiles, or a bound on them
+  bool tall;                 // row tiles of 256 with 128 for what is left, or of 128
 };
+
+// Tile of workgroup blk.  Workgroups go to the 8 XCDs in turn and an XCD runs 32 of
+// these at a time, so of every 256 each XCD gets 32 that lie together: kPanel row
+// tiles by 32 / kPanel column tiles, which share their operands in its cache.
+constexpr int kPanel = 4;
+__device__ __forceinline__ void place_tile(const Fp8Args& p, int64_t blk, int& mt, int& nt) {
+  const int64_t total = p.m_tiles * p.n_tiles, base = blk & ~int64_t(255);
+  const int count = (int)min(total - base, (int64_t)256), i = (int)(blk - base), x = i & 7;
+  const int64_t id = base + x * (count >> 3) + min(x, count & 7) + (i >> 3);
+  const int64_t panel = id / (kPanel * p.n_tiles);
+  const int in = (int)(id - panel * kPanel * p.n_tiles), high = (int)min(p.m_tiles - panel * kPanel, (int64_t)kPanel);
+  nt = in / high;
+  mt = (int)(panel * kPanel) + in % high;
+}
+
+// Row tile mt: the shard, its first row and the shard's end; `half`: it has 128 rows
+// and not 256.  Whole tiles of all shards (tall: a rest over 128 rows is one) come
+// first, then the halves, which even out the end of the launch.  False past the
+// last tile.  The result is the same in every lane.
+__device__ __forceinline__ bool locate_mixed(const Fp8Args& p, int mt, int& e, int& row0, int& row_end, bool& half) {
+  const int lane = threadIdx.x & 63, experts = p.offsets ? p.experts : 1;
+  half = false;
+#pragma unroll 1
+  for (int pass = p.tall ? 0 : 1; pass < 2; ++pass) {
+    int base = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < experts; e0 += 64) {
+      int lo = 0, hi = 0;
+      if (e0 + lane < experts) {
+        if (p.offsets) shard_bounds(p.offsets, e0 + lane, (int)p.tokens, lo, hi);
+        else hi = (int)p.tokens;
+      }
+      const int n = hi - lo, whole = (n + 127) >> 8;   // of 256 rows, a rest over 128 among them
+      const int own = pass == 0 ? whole : (p.tall ? (n > whole << 8 ? 1 : 0) : (n + 127) >> 7);
+      int sum = own;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(sum, d);
+        if (lane >= d) sum += v;
+      }
+      const int total = __builtin_amdgcn_readlane(sum, 63);
+      if (mt < base + total) {
+        const int src = __builtin_ctzll(__ballot(base + sum > mt));
+        const int nth = mt - base - __builtin_amdgcn_readlane(sum, src) + __builtin_amdgcn_readlane(own, src);
+        e = e0 + src;
+        half = pass == 1;
+        row0 = __builtin_amdgcn_readlane(lo, src);
+        row0 += half ? (p.tall ? __builtin_amdgcn_readlane(whole, src) << 8 : nth << 7) : nth << 8;
+        row_end = __builtin_amdgcn_readlane(hi, src);
+        return true;
+      }
+      base += total;
+    }
+    mt -= base;
+  }
+  return false;
+}
 
 constexpr int kE4M3 = 0;   // the scaled instruction's operand format field
 
@@ -291,16 +350,17 @@ void launch_exact_tiles(Fp8Args p, int out_dtype, hipStream_t st) {
 // One workgroup of four waves owns 256 columns of W by 64 FM tokens, each wave 128
 // by 32 FM in 32 x 32 x 64 scaled instructions (lane l: row l % 32, the 32 k of
 // group l / 32; D's lane l: column l % 32, rows 8 (i / 4) + 4 (l / 32) + i % 4).
-// k runs in halves of a scale block, 64 bytes of every row, through a ring of four
-// buffers in LDS: while half h is multiplied from registers, the fragments of h + 1
-// are read, h + 2 and h + 3 are on their way and h + 4 is asked for, into the
-// buffer that h left.  A row's four 16-byte chunks lie at position chunk ^ (row / 4
-// % 4): 16 rows of a fragment read then take every bank once.
+// A stage is a scale block of 128 k: whole lines of 128 bytes of every row go to
+// LDS with direct loads, two stages in turn.  While one half of a stage is
+// multiplied from registers the next half's fragments are read; once a stage's
+// second half is read, the waves meet, and the stage after the next is asked for.
+// A row's eight 16-byte chunks lie at position chunk ^ (row / 2 % 8): 16 rows of a
+// fragment read take every bank once.
 template <int FM>
 struct Fp8TileShared {
-  uint8_t w[4][256 * 64];
-  uint8_t x[4][64 * FM * 64];
-  // scales of eight stages of 128 k: bytes of rows r, r + 32, .. of a wave's half
+  uint8_t w[2][256 * 128];
+  uint8_t x[2][64 * FM * 128];
+  // scales of eight stages: bytes of rows r, r + 32, .. of a wave's half
   uint32_t ws[8][2][32], xs[8][2][32];
 };
 
@@ -310,41 +370,37 @@ __device__ __forceinline__ f32x16 mfma_fp8(const Frag<true>& a, const Frag<true>
 }
 
 template <int FM>
-__global__ __launch_bounds__(256, 1) void fp8_tiles_kernel(Fp8Args p, int64_t blk0) {
-  constexpr int FN = 4, BM = 64 * FM, kAll = FN * FM, kLoads = FN + FM;
-  __shared__ __align__(16) union {
-    Fp8TileShared<FM> t;
-    uint8_t out[4][quarter_bytes<FN, true>()];
-  } sh;
+union Fp8TileMemory {
+  Fp8TileShared<FM> t;
+  uint8_t out[4][quarter_bytes<4, true>()];
+};
+template <int FM>
+__device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM>& sh, int e, int row0, int row_end,
+                                         int nt) {
+  constexpr int FN = 4, BM = 64 * FM, kAll = FN * FM, kLoads = 2 * (FN + FM);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t blk = (int64_t)blockIdx.x + blk0;
-  const int nt = (int)(blk % p.n_tiles), mt = (int)(blk / p.n_tiles);
-  int e = 0, row0 = p.offsets ? 0 : mt * BM, row_end = (int)p.tokens;
-  if (p.offsets) {
-    if (!locate_tile<BM>(p.offsets, p.experts, (int)p.tokens, mt, e, row0, row_end)) return;
-  }
-  const int n0 = nt * 256, stages = p.k >> 7, halves = 2 * stages;
+  const int n0 = nt * 256, stages = p.k >> 7;
   const int wrows = p.n - n0, xrows = row_end - row0;
   const uint8_t* w = p.w + ((int64_t)e * p.n + n0) * p.k;
   const uint8_t* x = p.a + (int64_t)row0 * p.k;
   const int wn = wave & 1, wm = wave >> 1;   // this wave's quarter
 
-  // Direct loads: an instruction covers 16 rows; lane l is row l / 4, position l % 4.
-  const int ch = (lane & 3) ^ (lane >> 4);
-  uint32_t wo[FN], xo[FM];
+  // Direct loads: an instruction covers 8 rows; lane l is row l / 8, position l % 8.
+  auto ch = [&](int i) { return (lane & 7) ^ (((i & 1) << 2) | (lane >> 4)); };
+  uint32_t wo[2 * FN], xo[2 * FM];
 #pragma unroll
-  for (int i = 0; i < FN; ++i)
-    wo[i] = (uint32_t)min(16 * (wave * FN + i) + (lane >> 2), wrows - 1) * (uint32_t)p.k + ch * 16;
+  for (int i = 0; i < 2 * FN; ++i)
+    wo[i] = (uint32_t)min(8 * (wave * 2 * FN + i) + (lane >> 3), wrows - 1) * (uint32_t)p.k + ch(i) * 16;
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
-    xo[i] = (uint32_t)min(16 * (wave * FM + i) + (lane >> 2), xrows - 1) * (uint32_t)p.k + ch * 16;
+  for (int i = 0; i < 2 * FM; ++i)
+    xo[i] = (uint32_t)min(8 * (wave * 2 * FM + i) + (lane >> 3), xrows - 1) * (uint32_t)p.k + ch(i) * 16;
   const buffer_t wb = buffer_of(w, (int64_t)min(wrows, 256) * p.k);
   const buffer_t xb = buffer_of(x, (int64_t)min(xrows, BM) * p.k);
-  auto fetch = [&](auto b, int h, int i) {   // past the end the last half again, which nobody reads
-    constexpr int B = decltype(b)::value & 3;
-    const uint32_t so = (uint32_t)min(h, halves - 1) * 64;
-    if (i < FN) load_to_lds(wb, wo[i < FN ? i : 0], so, &sh.t.w[B][(wave * FN + i) * 1024]);
-    else load_to_lds(xb, xo[i < FN ? 0 : i - FN], so, &sh.t.x[B][(wave * FM + i - FN) * 1024]);
+  auto fetch = [&](auto b, int s, int i) {   // past the end the last stage again, which nobody reads
+    constexpr int B = decltype(b)::value & 1;
+    const uint32_t so = (uint32_t)min(s, stages - 1) * 128;
+    if (i < 2 * FN) load_to_lds(wb, wo[i < 2 * FN ? i : 0], so, &sh.t.w[B][(wave * 2 * FN + i) * 1024]);
+    else load_to_lds(xb, xo[i < 2 * FN ? 0 : i - 2 * FN], so, &sh.t.x[B][(wave * 2 * FM + i - 2 * FN) * 1024]);
   };
   // Scales, four stages at a time: thread t those of row t of either operand.
   const float* ws = p.w_scales + ((int64_t)e * p.scale_rows + ((n0 + min(tid, wrows - 1)) >> p.scale_shift)) * stages;
@@ -379,16 +435,23 @@ __global__ __launch_bounds__(256, 1) void fp8_tiles_kernel(Fp8Args p, int64_t bl
   };
   Step step[2];
   int wsc, xsc, wsn, xsn;   // scale words of this stage and the next
-  const int c0 = ((2 * g) ^ ((r >> 2) & 3)) * 16;
-  const uint8_t *wl = &sh.t.w[0][(wn * 128 + r) * 64], *xl = &sh.t.x[0][(wm * 32 * FM + r) * 64];
-  // Piece i of the fragments of a half in buffer B: both chunks of fragment i / 2.
-  auto read = [&](auto b, int i, Step& o) {
-    constexpr int B = decltype(b)::value & 3;
-    const int f = i >> 1, c = (i & 1) ? c0 ^ 16 : c0;
+  const uint8_t *wl[2], *xl[2];   // this lane's first chunk of its first fragment, for either half
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+    const int c = ((4 * ks + 2 * g) ^ ((r >> 1) & 7)) * 16;
+    wl[ks] = &sh.t.w[0][(wn * 128 + r) * 128 + c];
+    xl[ks] = &sh.t.x[0][(wm * 32 * FM + r) * 128 + c];
+  }
+  // Piece i of the fragments of half ks of the stage in buffer b: chunk i % 2 of
+  // fragment i / 2.  The second chunk is the first's neighbour, at position ^ 1.
+  const int flip = ((r >> 1) & 1) ? -16 : 16;
+  auto read = [&](auto b, int ks, int i, Step& o) {
+    constexpr int B = decltype(b)::value & 1;
+    const int f = i >> 1, c = (i & 1) ? flip : 0;
     i32x4& to = f < FN ? ((i & 1) ? o.w[f < FN ? f : 0].hi : o.w[f < FN ? f : 0].lo)
                        : ((i & 1) ? o.x[f < FN ? 0 : f - FN].hi : o.x[f < FN ? 0 : f - FN].lo);
-    to = f < FN ? *reinterpret_cast<const i32x4*>(wl + B * 256 * 64 + f * 32 * 64 + c)
-                : *reinterpret_cast<const i32x4*>(xl + B * BM * 64 + (f - FN) * 32 * 64 + c);
+    to = f < FN ? *reinterpret_cast<const i32x4*>(wl[ks] + c + B * 256 * 128 + f * 32 * 128)
+                : *reinterpret_cast<const i32x4*>(xl[ks] + c + B * BM * 128 + (f - FN) * 32 * 128);
   };
   auto read_scales = [&](int s) {
     wsn = (int)sh.t.ws[s & 7][wn][r];
@@ -396,37 +459,34 @@ __global__ __launch_bounds__(256, 1) void fp8_tiles_kernel(Fp8Args p, int64_t bl
   };
   f32x16 acc[FN][FM] = {};
 
-  constexpr int kPieces = 2 * kLoads, kPer = 2 * kPieces / kAll;   // read behind the first half of the products
-  constexpr int kWait = kAll == 16 ? 11 : 6;                       // the product behind which the waves meet
-  // Half h, in buffer h % 4 (Q, its place among eight, tells); SCALES: its share of
+  // Of the 2 kAll products of a stage: a half's 2 (FN + FM) pieces are read behind
+  // kRead of them, the waves meet behind product kMeet, loads follow from there.
+  constexpr int kPieces = 2 * (FN + FM), kRead = kAll == 16 ? 8 : 4, kPer = (kPieces + kRead - 1) / kRead;
+  constexpr int kMeet = kAll == 16 ? 11 : 6, kLoadPer = kAll == 16 ? 1 : 2;
+  // Stage s, in buffer Q % 2 (Q, its place among four, tells); SCALES: its share of
   // bringing the next four stages' scales.
-  auto half = [&](auto q, auto scales, int h) {
-    constexpr int Q = decltype(q)::value, B = Q & 3;
-    const Step& cur = step[B & 1];
-    Step& next = step[(B + 1) & 1];
-    if ((B & 1) == 0) {
-      wsc = wsn;
-      xsc = xsn;
-    }
-    unrolled<kAll>([&](auto idx) {
-      constexpr int i = decltype(idx)::value, I = i / FM, J = i % FM;
-      acc[I][J] = mfma_fp8<I, J>(cur.w[I], cur.x[J], acc[I][J], wsc, xsc);
-      if constexpr (i * kPer < kPieces) {
+  auto stage = [&](auto q, auto scales, int s) {
+    constexpr int Q = decltype(q)::value;
+    wsc = wsn;
+    xsc = xsn;
+    unrolled<2 * kAll>([&](auto idx) {
+      constexpr int i = decltype(idx)::value, I = i % kAll / FM, J = i % FM, ks = i / kAll, j = i % kAll;
+      acc[I][J] = mfma_fp8<I, J>(step[ks].w[I], step[ks].x[J], acc[I][J], wsc, xsc);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (i * kPer + j < kPieces) read(std::integral_constant<int, (B + 1) & 3>(), i * kPer + j, next);
-      }
-      if constexpr (i < kLoads) fetch(q, h + 4, i);
-      if constexpr (i == kLoads) {
-        if constexpr ((B & 1) == 1) read_scales((h + 1) >> 1);
-        if constexpr (decltype(scales)::value && Q == 0) fetch_scales((h >> 1) + 4);
-        if constexpr (decltype(scales)::value && Q == 4) put_scales((h >> 1) + 2);
-      }
-      if constexpr (i == kWait) {
-        // h + 1 is read, and of this wave's loads all but the last two halves' have landed
-        static_assert(kLoads == 8 || kLoads == 6, "vmcnt");
-        __builtin_amdgcn_s_waitcnt(kLoads == 8 ? 0x4070 : 0x007C);   // lgkmcnt(0), vmcnt(2 kLoads)
+      for (int c = j * kPer; c < (j + 1) * kPer; ++c)
+        if (c < kPieces) read(std::integral_constant<int, Q + ks>(), 1 - ks, c, step[1 - ks]);
+      if constexpr (i == kAll + kRead) read_scales(s + 1);
+      if constexpr (decltype(scales)::value && Q == 0 && i == kRead) fetch_scales(s + 4);
+      if constexpr (decltype(scales)::value && Q == 2 && i == kRead) put_scales(s + 2);
+      if constexpr (i == kMeet) {
+        // this stage is read, and the next has landed
+        __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0), lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
+      }
+      if constexpr (i > kMeet) {
+#pragma unroll
+        for (int c = (i - kMeet - 1) * kLoadPer; c < (i - kMeet) * kLoadPer; ++c)
+          if (c < kLoads) fetch(q, s + 2, c);
       }
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -438,38 +498,31 @@ __global__ __launch_bounds__(256, 1) void fp8_tiles_kernel(Fp8Args p, int64_t bl
       for (int j = 0; j < FM; ++j) asm volatile("" : "+a"(acc[i][j]));
   };
 
-  constexpr std::integral_constant<int, 0> b0{};
-  constexpr std::integral_constant<int, 1> b1{};
-  constexpr std::integral_constant<int, 2> b2{};
-  constexpr std::integral_constant<int, 3> b3{};
+  constexpr std::integral_constant<int, 0> q0{};
+  constexpr std::integral_constant<int, 1> q1{};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     wq[j] = __float_as_uint(ws[min(j, stages - 1)]);
     xq[j] = __float_as_uint(xs[min(j, stages - 1)]);
   }
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) fetch(b0, 0, i);
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) fetch(b1, 1, i);
+  for (int i = 0; i < kLoads; ++i) fetch(q0, 0, i);
   put_scales(0);
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) fetch(b2, 2, i);
+  for (int i = 0; i < kLoads; ++i) fetch(q1, 1, i);
+  static_assert(kLoads == 16 || kLoads == 12, "vmcnt");
+  __builtin_amdgcn_s_waitcnt(kLoads == 16 ? 0x4070 : 0x007C);   // vmcnt(kLoads), lgkmcnt(0): stage 0 has landed
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) fetch(b3, 3, i);
-  __builtin_amdgcn_s_waitcnt(kLoads == 8 ? 0x4070 : 0x007C);
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) read(b0, i, step[0]);
+  for (int i = 0; i < kPieces; ++i) read(q0, 0, i, step[0]);
   read_scales(0);
-  __syncthreads();   // all have read half 0: its buffer is free
-  int h = 0;
-  for (; h + 8 <= halves; h += 8) unrolled<8>([&](auto q) { half(q, std::true_type(), h + decltype(q)::value); });
-  for (; h < halves; h += 4) {
-    half(b0, std::false_type(), h);
-    half(b1, std::false_type(), h + 1);
-    if (h + 2 >= halves) break;
-    half(b2, std::false_type(), h + 2);
-    half(b3, std::false_type(), h + 3);
+  int s = 0;
+  for (; s + 4 <= stages; s += 4) unrolled<4>([&](auto q) { stage(q, std::true_type(), s + decltype(q)::value); });
+  for (; s < stages; s += 2) {
+    stage(q0, std::false_type(), s);
+    if (s + 1 >= stages) break;
+    stage(q1, std::false_type(), s + 1);
   }
   __builtin_amdgcn_s_waitcnt(0x0070);   // what was asked for past the end has landed too
   __syncthreads();
@@ -477,11 +530,26 @@ __global__ __launch_bounds__(256, 1) void fp8_tiles_kernel(Fp8Args p, int64_t bl
                               p.a_row_scale);
 }
 
-template <int FM>
+__global__ __launch_bounds__(256, 1) void fp8_tiles_kernel(Fp8Args p, int64_t blk0) {
+  __shared__ __align__(16) union {
+    Fp8TileMemory<4> whole;
+    Fp8TileMemory<2> half;
+  } sh;
+  int nt, mt, e, row0, row_end;
+  bool half;
+  place_tile(p, (int64_t)blockIdx.x + blk0, mt, nt);
+  if (!locate_mixed(p, mt, e, row0, row_end, half)) return;
+  if (half) fp8_tile<2>(p, sh.half, e, row0, row_end, nt);
+  else fp8_tile<4>(p, sh.whole, e, row0, row_end, nt);
+}
+
 void launch_tiles(Fp8Args p, hipStream_t st) {
+  const bool grouped = p.offsets != nullptr;
   p.n_tiles = (p.n + 255) / 256;
-  const int64_t blocks = p.n_tiles * max_row_tiles(p.tokens, p.experts, 64 * FM, p.offsets != nullptr);
-  launch_1d(fp8_tiles_kernel<FM>, blocks, 256, st, p);
+  p.m_tiles = max_row_tiles(p.tokens, p.experts, 256, grouped);
+  p.tall = p.m_tiles * p.n_tiles > 192;
+  if (!p.tall) p.m_tiles = max_row_tiles(p.tokens, p.experts, 128, grouped);
+  launch_1d(fp8_tiles_kernel, p.n_tiles * p.m_tiles, 256, st, p);
 }
 
 void launch_product(const Fp8Args& p, int out_dtype, hipStream_t st) {
@@ -493,9 +561,7 @@ void launch_product(const Fp8Args& p, int out_dtype, hipStream_t st) {
     if (p.tokens <= 16) launch_rows<1, 1, 8, 4>(p, out_dtype, st);
     else launch_rows<2, 2, 8, 2>(p, out_dtype, st);
   } else if (out_dtype == FP4_DTYPE_BF16) {
-    const int64_t wide = (int64_t)((p.n + 255) / 256) * max_row_tiles(p.tokens, p.experts, 128, grouped);
-    if (wide > 256 && (!grouped || per >= 256)) launch_tiles<4>(p, st);
-    else launch_tiles<2>(p, st);
+    launch_tiles(p, st);
   } else {
     launch_exact_tiles<2>(p, out_dtype, st);
   }
@@ -529,7 +595,7 @@ int product(const uint8_t* a, const float* a_scales, const float* a_row_scale, c
   for (int i = 0; i < 6; ++i)
     if (overlaps(out, n_out * osz, ins[i], inn[i])) return FP4_EOVERLAP;
   Fp8Args p = {a, a_scales, a_row_scale, w, w_scales, offsets, out, T, (int)E, (int)N, (int)K,
-               block_rows == 1 ? 0 : 7, (int)scale_rows, 0};
+               block_rows == 1 ? 0 : 7, (int)scale_rows, 0, 0, false};
   clear_stale_error();
   launch_product(p, out_dtype, as_stream(stream));
   return launch_status();

@@ -351,15 +351,16 @@ void launch_exact_tiles(Fp8Args p, int out_dtype, hipStream_t st) {
 // by 32 FM in 32 x 32 x 64 scaled instructions (lane l: row l % 32, the 32 k of
 // group l / 32; D's lane l: column l % 32, rows 8 (i / 4) + 4 (l / 32) + i % 4).
 // A stage is a scale block of 128 k: whole lines of 128 bytes of every row go to
-// LDS with direct loads, two stages in turn.  While one half of a stage is
+// LDS with direct loads, kBuffers stages in turn.  While one half of a stage is
 // multiplied from registers the next half's fragments are read; once a stage's
-// second half is read, the waves meet, and the stage after the next is asked for.
+// second half is read, the waves meet, and a later stage is asked for into its
+// buffer.
 // A row's eight 16-byte chunks lie at position chunk ^ (row / 2 % 8): 16 rows of a
 // fragment read take every bank once.
 template <int FM>
 struct Fp8TileShared {
-  uint8_t w[2][256 * 128];
-  uint8_t x[2][64 * FM * 128];
+  static constexpr int kBuffers = FM == 4 ? 2 : 3, kStage = (256 + 64 * FM) * 128;
+  uint8_t rows[kBuffers][kStage];   // W's, then A's
   // scales of eight stages: bytes of rows r, r + 32, .. of a wave's half
   uint32_t ws[8][2][32], xs[8][2][32];
 };
@@ -378,6 +379,7 @@ template <int FM>
 __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM>& sh, int e, int row0, int row_end,
                                          int nt) {
   constexpr int FN = 4, BM = 64 * FM, kAll = FN * FM, kLoads = 2 * (FN + FM);
+  constexpr int kBuffers = Fp8TileShared<FM>::kBuffers, kStage = Fp8TileShared<FM>::kStage;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n0 = nt * 256, stages = p.k >> 7;
   const int wrows = p.n - n0, xrows = row_end - row0;
@@ -396,11 +398,11 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM>& sh
     xo[i] = (uint32_t)min(8 * (wave * 2 * FM + i) + (lane >> 3), xrows - 1) * (uint32_t)p.k + ch(i) * 16;
   const buffer_t wb = buffer_of(w, (int64_t)min(wrows, 256) * p.k);
   const buffer_t xb = buffer_of(x, (int64_t)min(xrows, BM) * p.k);
-  auto fetch = [&](auto b, int s, int i) {   // past the end the last stage again, which nobody reads
-    constexpr int B = decltype(b)::value & 1;
+  auto fetch = [&](int at, int s, int i) {   // into buffer at; past the end the last stage again, which nobody reads
     const uint32_t so = (uint32_t)min(s, stages - 1) * 128;
-    if (i < 2 * FN) load_to_lds(wb, wo[i < 2 * FN ? i : 0], so, &sh.t.w[B][(wave * 2 * FN + i) * 1024]);
-    else load_to_lds(xb, xo[i < 2 * FN ? 0 : i - 2 * FN], so, &sh.t.x[B][(wave * 2 * FM + i - 2 * FN) * 1024]);
+    uint8_t* to = sh.t.rows[0] + at * kStage;
+    if (i < 2 * FN) load_to_lds(wb, wo[i < 2 * FN ? i : 0], so, to + (wave * 2 * FN + i) * 1024);
+    else load_to_lds(xb, xo[i < 2 * FN ? 0 : i - 2 * FN], so, to + 256 * 128 + (wave * 2 * FM + i - 2 * FN) * 1024);
   };
   // Scales, four stages at a time: thread t those of row t of either operand.
   const float* ws = p.w_scales + ((int64_t)e * p.scale_rows + ((n0 + min(tid, wrows - 1)) >> p.scale_shift)) * stages;
@@ -439,19 +441,18 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM>& sh
 #pragma unroll
   for (int ks = 0; ks < 2; ++ks) {
     const int c = ((4 * ks + 2 * g) ^ ((r >> 1) & 7)) * 16;
-    wl[ks] = &sh.t.w[0][(wn * 128 + r) * 128 + c];
-    xl[ks] = &sh.t.x[0][(wm * 32 * FM + r) * 128 + c];
+    wl[ks] = sh.t.rows[0] + (wn * 128 + r) * 128 + c;
+    xl[ks] = sh.t.rows[0] + (256 + wm * 32 * FM + r) * 128 + c;
   }
-  // Piece i of the fragments of half ks of the stage in buffer b: chunk i % 2 of
+  // Piece i of the fragments of half ks of the stage in buffer at: chunk i % 2 of
   // fragment i / 2.  The second chunk is the first's neighbour, at position ^ 1.
   const int flip = ((r >> 1) & 1) ? -16 : 16;
-  auto read = [&](auto b, int ks, int i, Step& o) {
-    constexpr int B = decltype(b)::value & 1;
-    const int f = i >> 1, c = (i & 1) ? flip : 0;
+  auto read = [&](int at, int ks, int i, Step& o) {
+    const int f = i >> 1, c = ((i & 1) ? flip : 0) + at * kStage;
     i32x4& to = f < FN ? ((i & 1) ? o.w[f < FN ? f : 0].hi : o.w[f < FN ? f : 0].lo)
                        : ((i & 1) ? o.x[f < FN ? 0 : f - FN].hi : o.x[f < FN ? 0 : f - FN].lo);
-    to = f < FN ? *reinterpret_cast<const i32x4*>(wl[ks] + c + B * 256 * 128 + f * 32 * 128)
-                : *reinterpret_cast<const i32x4*>(xl[ks] + c + B * BM * 128 + (f - FN) * 32 * 128);
+    to = f < FN ? *reinterpret_cast<const i32x4*>(wl[ks] + c + f * 32 * 128)
+                : *reinterpret_cast<const i32x4*>(xl[ks] + c + (f - FN) * 32 * 128);
   };
   auto read_scales = [&](int s) {
     wsn = (int)sh.t.ws[s & 7][wn][r];
@@ -459,34 +460,50 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM>& sh
   };
   f32x16 acc[FN][FM] = {};
 
-  // Of the 2 kAll products of a stage: a half's 2 (FN + FM) pieces are read behind
-  // kRead of them, the waves meet behind product kMeet, loads follow from there.
+  // Of the 2 kAll products of a stage: the second half's 2 (FN + FM) pieces are read
+  // behind kRead of them; behind product kMeet the waves have all read this stage,
+  // and the loads into its buffer follow, kLoadPer a product; behind product kLand
+  // the next stage has landed, and its first half is read.
   constexpr int kPieces = 2 * (FN + FM), kRead = kAll == 16 ? 8 : 4, kPer = (kPieces + kRead - 1) / kRead;
-  constexpr int kMeet = kAll == 16 ? 11 : 6, kLoadPer = kAll == 16 ? 1 : 2;
-  // Stage s, in buffer Q % 2 (Q, its place among four, tells); SCALES: its share of
-  // bringing the next four stages' scales.
+  constexpr int kMeet = kAll == 16 ? 11 : 6, kLoadPer = kAll == 16 ? 1 : 2, kLand = kAll == 16 ? 17 : 8;
+  int now = 0;   // the buffer of stage s
+  // Stage s, s % 4 = Q; SCALES: its share of bringing the next four stages' scales.
   auto stage = [&](auto q, auto scales, int s) {
     constexpr int Q = decltype(q)::value;
+    const int here = now;
+    now = now + 1 == kBuffers ? 0 : now + 1;
     wsc = wsn;
     xsc = xsn;
     unrolled<2 * kAll>([&](auto idx) {
-      constexpr int i = decltype(idx)::value, I = i % kAll / FM, J = i % FM, ks = i / kAll, j = i % kAll;
+      constexpr int i = decltype(idx)::value, I = i % kAll / FM, J = i % FM, ks = i / kAll;
       acc[I][J] = mfma_fp8<I, J>(step[ks].w[I], step[ks].x[J], acc[I][J], wsc, xsc);
+      if constexpr (i < kRead) {
 #pragma unroll
-      for (int c = j * kPer; c < (j + 1) * kPer; ++c)
-        if (c < kPieces) read(std::integral_constant<int, Q + ks>(), 1 - ks, c, step[1 - ks]);
-      if constexpr (i == kAll + kRead) read_scales(s + 1);
-      if constexpr (decltype(scales)::value && Q == 0 && i == kRead) fetch_scales(s + 4);
+        for (int c = i * kPer; c < (i + 1) * kPer; ++c)
+          if (c < kPieces) read(here, 1, c, step[1]);
+      }
+      if constexpr (i > kLand && i <= kLand + kRead) {
+#pragma unroll
+        for (int c = (i - kLand - 1) * kPer; c < (i - kLand) * kPer; ++c)
+          if (c < kPieces) read(now, 0, c, step[0]);
+      }
+      if constexpr (i == kLand + kRead) read_scales(s + 1);
+      if constexpr (decltype(scales)::value && Q == 0 && i == kLand + 1) fetch_scales(s + 4);
       if constexpr (decltype(scales)::value && Q == 2 && i == kRead) put_scales(s + 2);
       if constexpr (i == kMeet) {
-        // this stage is read, and the next has landed
-        __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0), lgkmcnt(0)
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+      }
+      if constexpr (i == kLand) {
+        constexpr int kNew = (kLand - kMeet - 1) * kLoadPer;
+        constexpr int kBehind = (kBuffers - 2) * kLoads + (kNew < kLoads ? kNew : kLoads);
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (kBehind & 15) | (kBehind >> 4) << 14);   // vmcnt
         __builtin_amdgcn_s_barrier();
       }
       if constexpr (i > kMeet) {
 #pragma unroll
         for (int c = (i - kMeet - 1) * kLoadPer; c < (i - kMeet) * kLoadPer; ++c)
-          if (c < kLoads) fetch(q, s + 2, c);
+          if (c < kLoads) fetch(here, s + kBuffers, c);
       }
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -506,16 +523,18 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM>& sh
     xq[j] = __float_as_uint(xs[min(j, stages - 1)]);
   }
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) fetch(q0, 0, i);
+  for (int i = 0; i < kLoads; ++i) fetch(0, 0, i);
   put_scales(0);
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) fetch(q1, 1, i);
-  static_assert(kLoads == 16 || kLoads == 12, "vmcnt");
-  __builtin_amdgcn_s_waitcnt(kLoads == 16 ? 0x4070 : 0x007C);   // vmcnt(kLoads), lgkmcnt(0): stage 0 has landed
+  for (int b = 1; b < kBuffers; ++b)
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) fetch(b, b, i);
+  constexpr int kBehind = (kBuffers - 1) * kLoads;
+  __builtin_amdgcn_s_waitcnt(0x0070 | (kBehind & 15) | (kBehind >> 4) << 14);   // stage 0 has landed
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) read(q0, 0, i, step[0]);
+  for (int i = 0; i < kPieces; ++i) read(0, 0, i, step[0]);
   read_scales(0);
   int s = 0;
   for (; s + 4 <= stages; s += 4) unrolled<4>([&](auto q) { stage(q, std::true_type(), s + decltype(q)::value); });

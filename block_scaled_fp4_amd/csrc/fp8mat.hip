@@ -92,12 +92,21 @@ __device__ __forceinline__ i32x8 words(const Frag<true>& f) {
 }
 
 // --------------------------------------------------------------- few rows
-// One workgroup owns 16 FN columns of W by 16 FM tokens; its W waves take the
-// steps of 128 k in turn, straight from memory to registers, U steps at a time
-// with the next U in flight, and add their sums through LDS.
-template <int FN, int FM, int W, int U, bool BF16>
+// One workgroup owns 16 FN columns of W by 16 FM tokens; each of its waves takes a
+// run of the steps of 128 k, and their sums meet in LDS.  A wave's rows come by
+// direct loads, a line of 128 bytes each, into NB buffers of its own, so it waits
+// for nobody.  (Straight to registers 16 lanes read 16 rows, and each costs the
+// cache a look-up: 64 tokens by 4096 x 4096 12.1 us so, 8.6 by way of LDS, 256 tokens
+// 42.6 and 13.4.)  Bound by memory where the weights are large: 64 tokens over 32
+// experts of 2048 x 7168 48 us, 5.5 TB/s; one token by 4096 x 7168 5.3 us.
+template <int FN, int FM, int W, int NB, bool BF16>
 __global__ __launch_bounds__(64 * W) void fp8_rows_product_kernel(Fp8Args p, int64_t blk0) {
-  __shared__ f32x4 red[W][FN * FM][64];
+  static_assert(8 % NB == 0, "eight steps end where they began");
+  constexpr int kLoads = 2 * (FN + FM), kStep = 16 * (FN + FM) * 128;
+  __shared__ __align__(16) union {
+    uint8_t rows[W][NB][kStep];   // W's, then A's; chunks placed as in the tiles below
+    f32x4 red[W][FN * FM][64];
+  } sh;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t blk = (int64_t)blockIdx.x + blk0;
   const int nt = (int)(blk % p.n_tiles), mt = (int)(blk / p.n_tiles);
@@ -106,94 +115,105 @@ __global__ __launch_bounds__(64 * W) void fp8_rows_product_kernel(Fp8Args p, int
     if (!locate_tile<16 * FM>(p.offsets, p.experts, (int)p.tokens, mt, e, row0, row_end)) return;
   }
   const int r = lane & 15, g = lane >> 4, n0 = nt * (16 * FN), steps = p.k >> 7;
-  const uint8_t* w = p.w + (int64_t)e * p.n * p.k + 32 * g;
-  const float* ws = p.w_scales + (int64_t)e * p.scale_rows * steps;
-  int wn[FN], am[FM];
+  const int wrows = min(p.n - n0, 16 * FN), xrows = min(row_end - row0, 16 * FM);
+  const buffer_t wb = buffer_of(p.w + ((int64_t)e * p.n + n0) * p.k, (int64_t)wrows * p.k);
+  const buffer_t xb = buffer_of(p.a + (int64_t)row0 * p.k, (int64_t)xrows * p.k);
+  uint32_t off[kLoads];
 #pragma unroll
-  for (int f = 0; f < FN; ++f) wn[f] = min(n0 + 16 * f + r, p.n - 1);
+  for (int i = 0; i < kLoads; ++i) {
+    const int row = 8 * (i < 2 * FN ? i : i - 2 * FN) + (lane >> 3);
+    off[i] = (uint32_t)min(row, (i < 2 * FN ? wrows : xrows) - 1) * (uint32_t)p.k +
+             (((lane & 7) ^ (((i & 1) << 2) | (lane >> 4))) << 4);
+  }
+  auto fetch = [&](int b, int c) {   // past the end the last step again, which nobody reads
 #pragma unroll
-  for (int f = 0; f < FM; ++f) am[f] = min(row0 + 16 * f + r, row_end - 1);
-
-  f32x4 acc[FN][FM] = {};
-  struct Batch {
-    LaneStep<true> w[U][FN], a[U][FM];
-  } even = {}, odd = {};   // in turn, so that no load is waited for before its use
+    for (int i = 0; i < kLoads; ++i)
+      load_to_lds(i < 2 * FN ? wb : xb, off[i], (uint32_t)min(c, steps - 1) * 128, &sh.rows[wave][b][i * 1024]);
+  };
+  // The scales of eight steps of each fragment's row, as bytes.
+  const float *ws[FN], *xs[FM];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+  for (int f = 0; f < FN; ++f)
+    ws[f] = p.w_scales + ((int64_t)e * p.scale_rows + ((n0 + min(16 * f + r, wrows - 1)) >> p.scale_shift)) * steps;
 #pragma unroll
-    for (int f = 0; f < FM; ++f) even.a[u][f].s = odd.a[u][f].s = 127;   // of lanes without a token
-  // U scales of a row from step c in one load where the row has them all
-  auto load_scales = [&](const float* row, int c, uint32_t (&s)[U]) {
-    if (c + U <= steps) {
-      memcpy(s, row + c, 4 * U);
+  for (int f = 0; f < FM; ++f) xs[f] = p.a_scales + (int64_t)(row0 + min(16 * f + r, xrows - 1)) * steps;
+  auto scales8 = [&](const float* row, int c, uint32_t (&out)[2]) {
+    uint32_t v[8];
+    const int at = min(c, steps - 8), past = c - at;
+    if (steps >= 8) {
+      memcpy(v, row + at, 32);
     } else {
 #pragma unroll
-      for (int u = 0; u < U; ++u) s[u] = __float_as_uint(row[min(c + u, steps - 1)]);
+      for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(row[min(c + j, steps - 1)]);
     }
+    uint64_t all = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) all |= (uint64_t)((v[j] >> 23) & 0xFFu) << (8 * j);
+    if (steps >= 8) all >>= 8 * min(past, 7);
+    out[0] = (uint32_t)all;
+    out[1] = (uint32_t)(all >> 32);
   };
-  auto load = [&](int c, Batch& b) {
+
+  f32x4 acc[FN][FM] = {};
+  const uint8_t* mine = &sh.rows[wave][0][r * 128 + (((2 * g) ^ (r >> 1)) << 4)];
+  const int flip = (r & 2) ? -16 : 16;
+  const int c0 = wave * steps / W, c1 = (wave + 1) * steps / W;
+  if (c0 < c1) {
 #pragma unroll
-    for (int f = 0; f < FN; ++f) {
-      uint32_t sc[U];
-      load_scales(ws + (int64_t)(wn[f] >> p.scale_shift) * steps, c, sc);
+    for (int b = 0; b < NB; ++b) fetch(b, c0 + b);
+  }
+  for (int c = c0; c < c1; c += 8) {
+    uint32_t wq[FN][2], xq[FM][2];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const i32x4* q = reinterpret_cast<const i32x4*>(w + (int64_t)wn[f] * p.k + min(c + u, steps - 1) * 128);
-        b.w[u][f].v.lo = q[0];
-        b.w[u][f].v.hi = q[1];
-        b.w[u][f].s = (int)((sc[u] >> 23) & 0xFFu);
-      }
-    }
+    for (int f = 0; f < FN; ++f) scales8(ws[f], c, wq[f]);
 #pragma unroll
-    for (int f = 0; f < FM; ++f) {
-      if (FM <= 2 && row0 + 16 * f + r >= row_end) continue;
-      uint32_t sc[U];
-      load_scales(p.a_scales + (int64_t)am[f] * steps, c, sc);
+    for (int f = 0; f < FM; ++f) scales8(xs[f], c, xq[f]);
+    unrolled<8>([&](auto step) {
+      constexpr int S = decltype(step)::value, B = S % NB;
+      if (c + S >= c1) return;
+      constexpr int kBehind = (NB - 1) * kLoads;
+      __builtin_amdgcn_s_waitcnt(0x0F70 | (kBehind & 15) | (kBehind >> 4) << 14);   // vmcnt: this step has landed
+      __builtin_amdgcn_wave_barrier();
+      LaneStep<true> w[FN], x[FM];
+      auto read = [&](int i, Frag<true>& v) {
+        v.lo = *reinterpret_cast<const i32x4*>(mine + B * kStep + i * 16 * 128);
+        v.hi = *reinterpret_cast<const i32x4*>(mine + flip + B * kStep + i * 16 * 128);
+      };
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const i32x4* q = reinterpret_cast<const i32x4*>(p.a + (int64_t)am[f] * p.k + min(c + u, steps - 1) * 128 + 32 * g);
-        b.a[u][f].v.lo = q[0];
-        b.a[u][f].v.hi = q[1];
-        b.a[u][f].s = (int)((sc[u] >> 23) & 0xFFu);
-      }
-    }
-  };
-  auto multiply = [&](int c, const Batch& b) {
+      for (int f = 0; f < FN; ++f) read(f, w[f].v);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (c + u >= steps) continue;
-      if constexpr (!BF16) {
-        mfma_bf16_step(b.w[u], b.a[u], acc);
-      } else {
+      for (int f = 0; f < FM; ++f) read(FN + f, x[f].v);
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): read, and free for the next
+      __builtin_amdgcn_wave_barrier();
+      fetch(B, c + S + NB);
+      if constexpr (BF16) {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
           for (int j = 0; j < FM; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                words(b.w[u][i].v), words(b.a[u][j].v), acc[i][j], kE4M3, kE4M3, 0, b.w[u][i].s, 0, b.a[u][j].s);
+                words(w[i].v), words(x[j].v), acc[i][j], kE4M3, kE4M3, S & 3, (int)wq[i][S >> 2], S & 3, (int)xq[j][S >> 2]);
+      } else {
+#pragma unroll
+        for (int f = 0; f < FN; ++f) w[f].s = (int)((wq[f][S >> 2] >> (8 * (S & 3))) & 0xFFu);
+#pragma unroll
+        for (int f = 0; f < FM; ++f) x[f].s = (int)((xq[f][S >> 2] >> (8 * (S & 3))) & 0xFFu);
+        mfma_bf16_step(w, x, acc);
       }
-    }
-  };
-  int c = wave * U;
-  constexpr int S = W * U;
-  if (c < steps) load(c, even);
-  for (; c < steps; c += 2 * S) {
-    if (c + S < steps) load(c + S, odd);
-    multiply(c, even);
-    if (c + S >= steps) break;
-    if (c + 2 * S < steps) load(c + 2 * S, even);
-    multiply(c + S, odd);
+    });
   }
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // what was asked for past the end has landed too
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int j = 0; j < FM; ++j) red[wave][i * FM + j][lane] = acc[i][j];
+    for (int j = 0; j < FM; ++j) sh.red[wave][i * FM + j][lane] = acc[i][j];
   __syncthreads();
   for (int s = threadIdx.x; s < FN * FM * 64; s += 64 * W) {
     const int f = s >> 6, l = s & 63;
-    f32x4 v = red[0][f][l];
+    f32x4 v = sh.red[0][f][l];
 #pragma unroll
-    for (int q = 1; q < W; ++q) v += red[q][f][l];
+    for (int q = 1; q < W; ++q) v += sh.red[q][f][l];
     const int m = row0 + 16 * (f % FM) + (l & 15), n = n0 + 16 * (f / FM) + 4 * (l >> 4);
     if (m < row_end && n < p.n) {
       if (p.a_row_scale) v *= p.a_row_scale[m];
@@ -202,17 +222,14 @@ __global__ __launch_bounds__(64 * W) void fp8_rows_product_kernel(Fp8Args p, int
   }
 }
 
-template <int FN, int FM, int W, int U>
-void launch_rows(Fp8Args p, int out_dtype, hipStream_t st) {
+template <int FN, int FM, int W, int NB, bool BF16>
+void launch_rows(Fp8Args p, hipStream_t st) {
   p.n_tiles = (p.n + 16 * FN - 1) / (16 * FN);
   const int64_t blocks = p.n_tiles * max_row_tiles(p.tokens, p.experts, 16 * FM, p.offsets != nullptr);
-  if (out_dtype == FP4_DTYPE_BF16)
-    launch_1d(fp8_rows_product_kernel<FN, FM, W, U, true>, blocks, 64 * W, st, p);
-  else
-    launch_1d(fp8_rows_product_kernel<FN, FM, W, U, false>, blocks, 64 * W, st, p);
+  launch_1d(fp8_rows_product_kernel<FN, FM, W, NB, BF16>, blocks, 64 * W, st, p);
 }
 
-// ---------------------------------------------- many rows, exact products
+// ------------------------------------------------------------- many rows
 // What the rare path of a tile needs, from the tile's first rows.
 struct Fp8View {
   const uint8_t *x, *w;
@@ -267,15 +284,14 @@ __device__ __forceinline__ void load_step(const uint8_t* row, const float* scale
   o.v.hi = q[1];
   o.s = (int)e8m0_of(scales[s]);
 }
-// A wave's 128 x 64 of a tile, 16 x 16 at a time straight from memory, for scales
-// of any range.  Out of line, like the above, so that it costs the common path no
-// registers.
-template <bool BF16>
-__device__ __attribute__((noinline)) void rare_quarter(Fp8View v, int mw, int nw, void* out,
+// 128 columns by `rows` tokens of a tile, 16 x 16 at a time straight from memory, for
+// scales of any range.  Out of line, like the above, so that it costs the common
+// path no registers.
+__device__ __attribute__((noinline)) void rare_quarter(Fp8View v, int mw, int rows, int nw, void* out,
                                                        int64_t out_row, int n_cols, const float* row_scale) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
 #pragma unroll 1
-  for (int i = 0; i < 32; ++i) {
+  for (int i = 0; i < rows / 2; ++i) {
     const int m = mw + (i >> 3) * 16, n = nw + (i & 7) * 16;
     const int wr = min(n + r, v.wrows - 1), xr = min(m + r, v.xrows - 1);
     LaneStep<true> lw[1], lx[1];
@@ -288,65 +304,11 @@ __device__ __attribute__((noinline)) void rare_quarter(Fp8View v, int mw, int nw
     }
     if (m + r < v.xrows) {
       if (row_scale) c[0][0] *= row_scale[out_row + m + r];
-      store_out4<BF16>(out, out_row + m + r, n_cols, v.n0 + n + 4 * g, c[0][0]);
+      store_out4<false>(out, out_row + m + r, n_cols, v.n0 + n + 4 * g, c[0][0]);
     }
   }
 }
 
-// See bf16_tile: W's rows are its operand A.
-template <int WM, bool BF16>
-__global__ __launch_bounds__(128 * WM, 1) void fp8_exact_tiles_kernel(Fp8Args p, int64_t blk0) {
-  constexpr int kBM = 64 * WM, T = 128 * WM;
-  __shared__ __align__(16) union {
-    Bf16Shared<true, WM> t;
-    uint8_t out[2 * WM][quarter_bytes<4, BF16>()];
-  } sh;
-  const int64_t blk = (int64_t)blockIdx.x + blk0;
-  const int nt = (int)(blk % p.n_tiles), mt = (int)(blk / p.n_tiles);
-  int e = 0, row0 = p.offsets ? 0 : mt * kBM, row_end = (int)p.tokens;
-  if (p.offsets) {
-    if (!locate_tile<kBM>(p.offsets, p.experts, (int)p.tokens, mt, e, row0, row_end)) return;
-  }
-  const int n0 = nt * kBN, kx = p.k >> 7;
-  const Fp8View v = {p.a + (int64_t)row0 * p.k, p.w + ((int64_t)e * p.n + n0) * p.k,
-                     p.a_scales + (int64_t)row0 * kx, p.w_scales + (int64_t)e * p.scale_rows * kx,
-                     p.k, row_end - row0, p.n - n0, n0, p.scale_shift};
-  constexpr int kLW = kBN * 8 / T, kLX = kBM * 8 / T;
-  uint32_t wo[kLW], xo[kLX];
-  const int tid = threadIdx.x;
-#pragma unroll
-  for (int i = 0; i < kLW; ++i)
-    wo[i] = (uint32_t)min((tid >> 3) + T / 8 * i, v.wrows - 1) * (uint32_t)p.k + (tid & 7) * 16;
-#pragma unroll
-  for (int i = 0; i < kLX; ++i)
-    xo[i] = (uint32_t)min((tid >> 3) + T / 8 * i, v.xrows - 1) * (uint32_t)p.k + (tid & 7) * 16;
-  f32x16 acc[4][2] = {};
-  const bool odd = bf16_tile<true, WM>(
-      sh.t, kx, kx,
-      [&](auto, int s, int i) { return *reinterpret_cast<const i32x4*>(v.w + s * 128 + wo[i]); },
-      [&](auto, int s, int i) { return *reinterpret_cast<const i32x4*>(v.x + s * 128 + xo[i]); },
-      [](int, int, i32x4&) {}, [](int, int, i32x4&) {},
-      [&](int s, int row) { return e8m0_of(weight_scales(v, min(row, v.wrows - 1))[s]); },
-      [&](int s, int row) { return e8m0_of(v.xs[(int64_t)min(row, v.xrows - 1) * kx + s]); }, acc);
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), mw = (wave >> 1) * 64, nw = (wave & 1) * 128;
-  if (__syncthreads_or(odd) && __syncthreads_or(scales_need_care<kBM>(v))) {
-    rare_quarter<BF16>(v, mw, nw, p.out, row0, p.n, p.a_row_scale);
-    return;
-  }
-  store_quarter<4, 2, BF16>(acc, sh.out[wave], p.out, row0 + mw, row_end, p.n, n0 + nw, p.a_row_scale);
-}
-
-template <int WM>
-void launch_exact_tiles(Fp8Args p, int out_dtype, hipStream_t st) {
-  p.n_tiles = (p.n + kBN - 1) / kBN;
-  const int64_t blocks = p.n_tiles * max_row_tiles(p.tokens, p.experts, 64 * WM, p.offsets != nullptr);
-  if (out_dtype == FP4_DTYPE_BF16)
-    launch_1d(fp8_exact_tiles_kernel<WM, true>, blocks, 128 * WM, st, p);
-  else
-    launch_1d(fp8_exact_tiles_kernel<WM, false>, blocks, 128 * WM, st, p);
-}
-
-// ------------------------------------------------ many rows, bf16 outputs
 // One workgroup of four waves owns 256 columns of W by 64 FM tokens, each wave 128
 // by 32 FM in 32 x 32 x 64 scaled instructions (lane l: row l % 32, the 32 k of
 // group l / 32; D's lane l: column l % 32, rows 8 (i / 4) + 4 (l / 32) + i % 4).
@@ -357,6 +319,11 @@ void launch_exact_tiles(Fp8Args p, int out_dtype, hipStream_t st) {
 // buffer.
 // A row's eight 16-byte chunks lie at position chunk ^ (row / 2 % 8): 16 rows of a
 // fragment read take every bank once.
+// For fp32 outputs (BF16 false) four 32 x 32 x 16 products of bf16 values, which hold
+// code times scale exactly, take the place of a scaled one.  Their time is that of
+// the products (twice the scaled one's) and of the conversions, which do not run
+// beside them (16 cycles each, as many for two products as one takes; spread evenly
+// between the products they cost the same).
 template <int FM>
 struct Fp8TileShared {
   static constexpr int kBuffers = FM == 4 ? 2 : 3, kStage = (256 + 64 * FM) * 128;
@@ -370,13 +337,13 @@ __device__ __forceinline__ f32x16 mfma_fp8(const Frag<true>& a, const Frag<true>
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(words(a), words(b), c, kE4M3, kE4M3, SA, sa, SB, sb);
 }
 
-template <int FM>
+template <int FM, bool BF16>
 union Fp8TileMemory {
   Fp8TileShared<FM> t;
-  uint8_t out[4][quarter_bytes<4, true>()];
+  uint8_t out[4][quarter_bytes<4, BF16>()];
 };
-template <int FM>
-__device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM>& sh, int e, int row0, int row_end,
+template <int FM, bool BF16>
+__device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM, BF16>& sh, int e, int row0, int row_end,
                                          int nt) {
   constexpr int FN = 4, BM = 64 * FM, kAll = FN * FM, kLoads = 2 * (FN + FM);
   constexpr int kBuffers = Fp8TileShared<FM>::kBuffers, kStage = Fp8TileShared<FM>::kStage;
@@ -413,10 +380,15 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM>& sh
     memcpy(&wq, ws + at, 16);
     memcpy(&xq, xs + at, 16);
   };
+  bool odd = false;   // some scale is outside the bf16 window
   auto put_scales = [&](int s) {
     const int past = min(max(s - max(stages - 4, 0), 0), 3);   // stages past the end get any scale
     const auto pack = [&](u32x4& v) {
       asm volatile("" : "+v"(v));   // else each is loaded as its upper half alone
+      if constexpr (!BF16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) odd |= !scale_in_window((int)(v[j] >> 23 & 0xFFu));
+      }
       const uint32_t lo = (v[0] >> 23 & 0xFFu) | (v[1] >> 15 & 0xFF00u);
       const uint32_t all = lo | (v[2] >> 7 & 0xFF0000u) | (v[3] << 1 & 0xFF000000u);
       return all >> (8 * past);
@@ -467,6 +439,22 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM>& sh
   constexpr int kPieces = 2 * (FN + FM), kRead = kAll == 16 ? 8 : 4, kPer = (kPieces + kRead - 1) / kRead;
   constexpr int kMeet = kAll == 16 ? 11 : 6, kLoadPer = kAll == 16 ? 1 : 2, kLand = kAll == 16 ? 17 : 8;
   int now = 0;   // the buffer of stage s
+  // Exact products, four in the place of one scaled: place i of a half has quarter
+  // i / FM, and of its FN FM products number 4 (i % FM) to + 3.  y: A's operands of
+  // this quarter and the next, v: W's of this place and the next.
+  constexpr int kOwn = 4 / FM;
+  bf16x8_t y[2][FM], v[2][kOwn];
+  auto scale_byte = [](int word, int f) { return scale_of((word >> (8 * f)) & 0xFF); };
+  auto to_y = [&](auto quarter, int f, const Step& o, int scales) {
+    constexpr int Q4 = decltype(quarter)::value;
+    y[Q4 & 1][f] = bf16_of<Q4>(o.x[f], scale_byte(scales, f));
+  };
+  auto to_v = [&](auto place, const Step& o, int scales) {
+    constexpr int i = decltype(place)::value;
+#pragma unroll
+    for (int d = 0; d < kOwn; ++d)
+      v[i & 1][d] = bf16_of<i / FM>(o.w[i % FM * kOwn + d], scale_byte(scales, i % FM * kOwn + d));
+  };
   // Stage s, s % 4 = Q; SCALES: its share of bringing the next four stages' scales.
   auto stage = [&](auto q, auto scales, int s) {
     constexpr int Q = decltype(q)::value;
@@ -475,8 +463,22 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM>& sh
     wsc = wsn;
     xsc = xsn;
     unrolled<2 * kAll>([&](auto idx) {
-      constexpr int i = decltype(idx)::value, I = i % kAll / FM, J = i % FM, ks = i / kAll;
-      acc[I][J] = mfma_fp8<I, J>(step[ks].w[I], step[ks].x[J], acc[I][J], wsc, xsc);
+      constexpr int i = decltype(idx)::value, ks = i / kAll, j = i % kAll;
+      if constexpr (BF16) {
+        constexpr int I = j / FM, J = j % FM;
+        acc[I][J] = mfma_fp8<I, J>(step[ks].w[I], step[ks].x[J], acc[I][J], wsc, xsc);
+      } else {
+        constexpr int q4 = j / FM, t = j % FM, next = (j + 1) % kAll;
+        constexpr bool later = i == 2 * kAll - 1;   // the next place is the next stage's
+        constexpr bool turn = q4 == 3;              // the next quarter is the next half's
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int I = (4 * t + c) / FM, J = (4 * t + c) % FM;
+          acc[I][J] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[j & 1][I - t * kOwn], y[q4 & 1][J], acc[I][J], 0, 0, 0);
+        }
+        to_v(std::integral_constant<int, next>(), step[j + 1 == kAll ? 1 - ks : ks], later ? wsn : wsc);
+        to_y(std::integral_constant<int, (q4 + 1) & 3>(), t, step[turn ? 1 - ks : ks], turn && ks == 1 ? xsn : xsc);
+      }
       if constexpr (i < kRead) {
 #pragma unroll
         for (int c = i * kPer; c < (i + 1) * kPer; ++c)
@@ -536,6 +538,11 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM>& sh
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) read(0, 0, i, step[0]);
   read_scales(0);
+  if constexpr (!BF16) {
+#pragma unroll
+    for (int f = 0; f < FM; ++f) to_y(std::integral_constant<int, 0>(), f, step[0], xsn);
+    to_v(std::integral_constant<int, 0>(), step[0], wsn);
+  }
   int s = 0;
   for (; s + 4 <= stages; s += 4) unrolled<4>([&](auto q) { stage(q, std::true_type(), s + decltype(q)::value); });
   for (; s < stages; s += 2) {
@@ -545,45 +552,71 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM>& sh
   }
   __builtin_amdgcn_s_waitcnt(0x0070);   // what was asked for past the end has landed too
   __syncthreads();
-  store_quarter<FN, FM, true>(acc, sh.out[wave], p.out, row0 + wm * 32 * FM, row_end, p.n, n0 + wn * 128,
+  if constexpr (!BF16) {
+    const Fp8View view = {x, w, p.a_scales + (int64_t)row0 * stages,
+                          p.w_scales + (int64_t)e * p.scale_rows * stages, p.k, min(xrows, BM), wrows, n0, p.scale_shift};
+    if (__syncthreads_or(odd) && __syncthreads_or(scales_need_care<BM>(view))) {
+      rare_quarter(view, wm * 32 * FM, 32 * FM, wn * 128, p.out, row0, p.n, p.a_row_scale);
+      return;
+    }
+  }
+  store_quarter<FN, FM, BF16>(acc, sh.out[wave], p.out, row0 + wm * 32 * FM, row_end, p.n, n0 + wn * 128,
                               p.a_row_scale);
 }
 
+template <bool BF16>
 __global__ __launch_bounds__(256, 1) void fp8_tiles_kernel(Fp8Args p, int64_t blk0) {
   __shared__ __align__(16) union {
-    Fp8TileMemory<4> whole;
-    Fp8TileMemory<2> half;
+    Fp8TileMemory<4, BF16> whole;
+    Fp8TileMemory<2, BF16> half;
   } sh;
   int nt, mt, e, row0, row_end;
   bool half;
   place_tile(p, (int64_t)blockIdx.x + blk0, mt, nt);
   if (!locate_mixed(p, mt, e, row0, row_end, half)) return;
-  if (half) fp8_tile<2>(p, sh.half, e, row0, row_end, nt);
-  else fp8_tile<4>(p, sh.whole, e, row0, row_end, nt);
+  if (half) fp8_tile<2, BF16>(p, sh.half, e, row0, row_end, nt);
+  else fp8_tile<4, BF16>(p, sh.whole, e, row0, row_end, nt);
 }
 
+template <bool BF16>
 void launch_tiles(Fp8Args p, hipStream_t st) {
   const bool grouped = p.offsets != nullptr;
   p.n_tiles = (p.n + 255) / 256;
   p.m_tiles = max_row_tiles(p.tokens, p.experts, 256, grouped);
   p.tall = p.m_tiles * p.n_tiles > 192;
   if (!p.tall) p.m_tiles = max_row_tiles(p.tokens, p.experts, 128, grouped);
-  launch_1d(fp8_tiles_kernel, p.n_tiles * p.m_tiles, 256, st, p);
+  launch_1d(fp8_tiles_kernel<BF16>, p.n_tiles * p.m_tiles, 256, st, p);
 }
 
-void launch_product(const Fp8Args& p, int out_dtype, hipStream_t st) {
+// Which kernel.  A few-row kernel's time hardly changes while each of its workgroups
+// has a compute unit to itself, and then grows with their number; the tiles' grows
+// with theirs only from there.  So the smallest few-row tile with 256 workgroups or
+// fewer is taken (4096 x 4096; us by columns x tokens of a workgroup, and tiles):
+//   1 token    16 x 16 4.5, 32 x 16 5.4, 32 x 32 6.3, 64 x 32 7.5, 64 x 64 9.5, tiles 24
+//   64 tokens  17.3, 13.6, 8.6, 8.7, 12.2, 25;  256 tokens  57, 46, 28, 16.6, 13.4, 25.
+// With more workgroups than that, weights are read once a row tile, so the tile's
+// tokens follow the tokens that there are, of a shard on average: up to a few 64 x 16
+// (16 tokens by 16384 x 4096 13.7, 64 x 32 14.9, 32 x 16 17.6; 64 tokens over 32
+// experts of 2048 x 4096 30.0, 33.5, 36.7), then 64 x 32 (256 tokens over the 32 46.8, 64 x
+// 64 51.8, tiles 43), 64 x 64 (1024 tokens 68.6, 64 x 32 72.9, tiles 76) and the tiles
+// (2048 tokens 87, 64 x 64 99).  With fp32 outputs the tiles take longer (512 tokens by
+// 4096 x 4096: 64 x 64 38, tiles 67, 1024 tokens 75 both; 4096 tokens over the 32: 191,
+// 273, 8192 tokens 349, 295).
+template <bool BF16>
+void launch_product(const Fp8Args& p, hipStream_t st) {
   const int64_t per = p.tokens / p.experts;
   const bool grouped = p.offsets != nullptr;
-  const int64_t small = (int64_t)((p.n + 31) / 32) * ((p.tokens + 31) / 32);
-  const bool tiles = grouped ? per >= 40 : small > 1600;
-  if (!tiles) {
-    if (p.tokens <= 16) launch_rows<1, 1, 8, 4>(p, out_dtype, st);
-    else launch_rows<2, 2, 8, 2>(p, out_dtype, st);
-  } else if (out_dtype == FP4_DTYPE_BF16) {
-    launch_tiles(p, st);
-  } else {
-    launch_exact_tiles<2>(p, out_dtype, st);
-  }
+  auto count = [&](int cols, int rows) {
+    return (int64_t)((p.n + cols - 1) / cols) * max_row_tiles(p.tokens, p.experts, rows, grouped);
+  };
+  if (count(16, 16) <= 256) return launch_rows<1, 1, 8, 2, BF16>(p, st);
+  if (count(32, 16) <= 256) return launch_rows<2, 1, 8, 2, BF16>(p, st);
+  if (grouped ? per <= 4 : p.tokens <= 16) return launch_rows<4, 1, 4, 2, BF16>(p, st);
+  if (count(32, 32) <= 256) return launch_rows<2, 2, 4, 4, BF16>(p, st);
+  if (count(64, 32) <= 256 || (grouped && per <= 24)) return launch_rows<4, 2, 4, 2, BF16>(p, st);
+  if (grouped ? per <= (BF16 ? 40 : 160) : count(64, 64) <= (BF16 ? 384 : 1024))
+    return launch_rows<4, 4, 4, 2, BF16>(p, st);
+  launch_tiles<BF16>(p, st);
 }
 
 // Checks shared by both products; experts == 0 stands for the plain one.
@@ -616,7 +649,8 @@ int product(const uint8_t* a, const float* a_scales, const float* a_row_scale, c
   Fp8Args p = {a, a_scales, a_row_scale, w, w_scales, offsets, out, T, (int)E, (int)N, (int)K,
                block_rows == 1 ? 0 : 7, (int)scale_rows, 0, 0, false};
   clear_stale_error();
-  launch_product(p, out_dtype, as_stream(stream));
+  if (out_dtype == FP4_DTYPE_BF16) launch_product<true>(p, as_stream(stream));
+  else launch_product<false>(p, as_stream(stream));
   return launch_status();
 }
 

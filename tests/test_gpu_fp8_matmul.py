@@ -124,6 +124,37 @@ def test_what_bf16_outputs_drop(m, n):
     R.assert_product(run(mod, qa.astype(np.uint8), one, qw.astype(np.uint8), np.ones((n, k // 128), np.float32), None, False), c, bound, False)
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("counts,n", [
+    ([3], 200), ([5], 4200), ([16], 8300), ([40], 3000), ([130], 2100), ([300], 2500), ([900], 4700),
+    ([1, 2, 0] * 20, 256), ([10] * 12, 1024), ([35] * 4, 2100), ([300, 0, 200, 520], 1030)])
+def test_long_rows(counts, n, bf16):
+    """K past what a wave or a stage group takes at once, for each kernel; reference
+    in fp64 on the GPU, the dropped products bounded by sum|a b|."""
+    mod = need_gpu()
+    k, E, T = 8448, len(counts), sum(counts)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + n)
+    a, sa = mod.fp8_quantize(torch.randn((T, k), generator=g, device="cuda"))
+    w, sw, _, _ = mod.fp8_quantize_blocks(torch.randn((E, n, k), generator=g, device="cuda"))
+    off = dev_i64(R.offsets_of(counts))
+    dt = torch.bfloat16 if bf16 else torch.float32
+    c = mod.fp8_matmul_grouped(a, sa, w, sw, off, out_dtype=dt) if E > 1 else mod.fp8_matmul(a, sa, w[0], sw[0], out_dtype=dt)
+
+    def wide(q, s):
+        return q.view(torch.float8_e4m3fn).double() * s.double().repeat_interleave(128, 1)
+    av = wide(a, sa)
+    for e in range(E):
+        t = slice(int(off[e]), int(off[e + 1]))
+        if counts[e]:
+            b = wide(w[e], sw[e].repeat_interleave(128, 0)[:n])
+            ref, mag = av[t] @ b.t(), av[t].abs() @ b.t().abs()
+            tol = ((k + 16) * R.U + (7 * 2.0 ** -13 if bf16 else 0)) * mag + (2.0 ** -8 if bf16 else R.U) * ref.abs()
+            assert bool(((c[t].double() - ref).abs() <= tol).all()), e
+            rms = float((c[t].double() - ref).norm() / ref.norm())      # Gaussian rows: what is dropped averages out
+            assert rms < (2.0 ** -8 if bf16 else 1e-6), rms
+
+
 def test_malformed_offsets_stay_inside():
     """Clamped on the device: rows outside every shard are not written."""
     mod = need_gpu()

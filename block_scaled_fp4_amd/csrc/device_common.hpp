@@ -98,6 +98,14 @@ __device__ __forceinline__ float lane_xor1(float v) {
 __device__ __forceinline__ float lane_xor2(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false));
 }
+// row_half_mirror and row_mirror: of values that are equal within each quad (each
+// eight), the other quad's of the eight (the other eight's of the sixteen).
+template <int CTRL>
+__device__ __forceinline__ uint32_t lane_dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+__device__ __forceinline__ float other_quad(float v) { return __uint_as_float(lane_dpp<0x141>(__float_as_uint(v))); }
+__device__ __forceinline__ float other_eight(float v) { return __uint_as_float(lane_dpp<0x140>(__float_as_uint(v))); }
 __device__ __forceinline__ int lane_xor1_i(int v) {
   return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, false);
 }

@@ -64,35 +64,47 @@ __device__ __forceinline__ void load_row(const void* base, int64_t row, int expe
   }
 }
 
+// f over the L lanes of a row, in every one of them, without LDS.
 template <int L, typename F>
 __device__ __forceinline__ float over_lanes(float v, F f) {
-#pragma unroll
-  for (int d = 1; d < L; d <<= 1) v = f(v, __shfl_xor(v, d));
+  v = f(v, lane_xor1(v));
+  v = f(v, lane_xor2(v));
+  v = f(v, other_quad(v));
+  if constexpr (L >= 16) v = f(v, other_eight(v));
+  if constexpr (L >= 32) {   // both halves of the pair, each in both
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  }
+  if constexpr (L >= 64) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  }
   return v;
 }
 
-// The softmax of a row in place.  A row of -inf alone becomes zeros; NaN and
-// +inf make the row NaN.
+// exp(x - max) of a row in place; returns the factor that makes them its softmax.  The
+// maximum is taken times log2(e), rounded: that moves all of a row alike, and x - max
+// is rounded once, in the fma.  A row of -inf alone becomes zeros; NaN and +inf make
+// the factor NaN.
 template <int L, int CH>
-__device__ __forceinline__ void softmax_row(f32x4 (&v)[CH]) {
+__device__ __forceinline__ float softmax_row(f32x4 (&v)[CH]) {
   float top = -INFINITY;
 #pragma unroll
   for (int c = 0; c < CH; ++c) top = fmaxf(fmaxf(fmaxf(v[c].x, v[c].y), fmaxf(v[c].z, v[c].w)), top);
   top = over_lanes<L>(top, [](float a, float b) { return fmaxf(a, b); });
-  if (top == -INFINITY) top = 0.0f;
+  constexpr float kLog2e = 0x1.715476p+0f;
+  const float m = top == -INFINITY ? 0.0f : top * kLog2e;
   float sum = 0.0f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[c][j] = exp_f32(v[c][j] - top);
+      v[c][j] = __builtin_amdgcn_exp2f(fmaf(v[c][j], kLog2e, -m));
       sum += v[c][j];
     }
   }
   sum = over_lanes<L>(sum, [](float a, float b) { return a + b; });
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-  for (int c = 0; c < CH; ++c) v[c] *= inv;
+  return sum == 0.0f ? 0.0f : 1.0f / sum;
 }
 
 struct BalanceArgs {
@@ -110,39 +122,75 @@ struct BalanceArgs {
   float* part_p;       // [blocks, E]
   int32_t* part_c;     // [blocks, E]
   int32_t* part_n;     // [blocks]
+  double* part_loss;   // [join blocks]
+  uint32_t* joined;    // join blocks that are done
   int blocks;
 };
 
-// A workgroup adds its rows' p in registers, row after row, its waves' sums in
-// LDS in the order of the waves, and leaves them, its counts and its number of
-// counted tokens in the workspace.
+// The sums of the counts before each expert, by one wave.
+template <typename F>
+__device__ __forceinline__ void write_offsets(const BalanceArgs& p, int lane, F count) {
+  int64_t base = 0;
+  for (int e0 = 0; e0 < p.experts; e0 += 64) {
+    const int own = e0 + lane < p.experts ? count(e0 + lane) : 0;
+    int sum = own;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(sum, d);
+      if (lane >= d) sum += v;
+    }
+    if (e0 + lane < p.experts) p.offsets[e0 + lane] = base + sum - own;
+    base += __builtin_amdgcn_readlane(sum, 63);
+  }
+  if (lane == 0) p.offsets[p.experts] = base;
+}
+
+// A workgroup adds its rows' p in registers, row after row, its waves' sums in the
+// order of the waves, and leaves them, its counts and its number of counted tokens in
+// the workspace.  A call of one workgroup ends here (1 token of 256 experts 5.3 us, with
+// the second launch 11).
+constexpr int kRowsAhead = 2;   // rows on their way
 template <bool BF16, bool IDX64, int L, int CH, int W>
 __global__ __launch_bounds__(64 * W) void balance_kernel(BalanceArgs p) {
-  constexpr int R = 64 / L;   // rows a wave takes at once
-  __shared__ float sums[L * CH * 4];
-  __shared__ int hist[L * CH * 4];
+  constexpr int R = 64 / L, kWide = L * CH * 4;   // rows a wave takes at once, columns
+  __shared__ f32x4 sums[W][kWide / 4];
+  __shared__ int hist[kWide];
   __shared__ int counted[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (L - 1), sub = lane / L;
-  for (int e = tid; e < L * CH * 4; e += 64 * W) {
-    sums[e] = 0.0f;
-    hist[e] = 0;
-  }
+  for (int e = tid; e < kWide; e += 64 * W) hist[e] = 0;
+  if (blockIdx.x == 0 && tid == 0) *p.joined = 0;
   __syncthreads();
-  f32x4 acc[CH] = {}, cur[CH], next[CH];
-  int n = 0;
+  constexpr int D = CH <= 2 ? kRowsAhead : 1;
+  f32x4 acc[CH] = {}, ahead[D][CH];
+  int n = 0, in[D];
   const int64_t step = (int64_t)p.blocks * W * R;
   int64_t row = ((int64_t)blockIdx.x * W + wave) * R + sub;
-  if (row < p.tokens) load_row<BF16, L, CH>(p.x, row, p.experts, l, -INFINITY, next);
-  for (; row < p.tokens; row += step) {
+  auto fetch = [&](int64_t at, int d) {
+    in[d] = 1;
+    if (at >= p.tokens) return;
+    load_row<BF16, L, CH>(p.x, at, p.experts, l, -INFINITY, ahead[d]);
+    if (p.mask) in[d] = p.mask[at];
+  };
 #pragma unroll
-    for (int c = 0; c < CH; ++c) cur[c] = next[c];
-    const bool in = !p.mask || p.mask[row];
-    if (row + step < p.tokens) load_row<BF16, L, CH>(p.x, row + step, p.experts, l, -INFINITY, next);
-    softmax_row<L, CH>(cur);
-    if (in) {   // not p times 0: a row that is not counted may hold anything
-      ++n;
+  for (int d = 0; d < D; ++d) fetch(row + d * step, d);
+  for (; row < p.tokens;) {
 #pragma unroll
-      for (int c = 0; c < CH; ++c) acc[c] += cur[c];
+    for (int d = 0; d < D; ++d) {
+      if (row >= p.tokens) continue;
+      f32x4 cur[CH];
+      const int counts = in[d];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) cur[c] = ahead[d][c];
+      fetch(row + D * step, d);
+      const float inv = softmax_row<L, CH>(cur);
+      if (counts) {   // not p times 0: a row that is not counted may hold anything
+        ++n;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[c][j] = fmaf(cur[c][j], inv, acc[c][j]);
+      }
+      row += step;
     }
   }
   for (int64_t s = (int64_t)blockIdx.x * (64 * W) + tid; s < p.slots; s += (int64_t)p.blocks * (64 * W)) {
@@ -159,95 +207,116 @@ __global__ __launch_bounds__(64 * W) void balance_kernel(BalanceArgs p) {
     n += __shfl_xor(n, d);
   }
   if (lane == 0) counted[wave] = n;
-  for (int w = 0; w < W; ++w) {
-    if (wave == w && sub == 0) {
+  if (sub == 0) {
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sums[4 * (c * L + l) + j] += acc[c][j];
-    }
-    __syncthreads();
+    for (int c = 0; c < CH; ++c) sums[wave][c * L + l] = acc[c];
   }
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) total += counted[w];
+  const bool whole = p.blocks == 1;
+  const double share = whole && total > 0 ? (double)p.coef * p.experts / ((double)p.k * total * total) : 0.0;
+  double loss = 0.0;
   for (int e = tid; e < p.experts; e += 64 * W) {
-    p.part_p[(int64_t)blockIdx.x * p.experts + e] = sums[e];
-    p.part_c[(int64_t)blockIdx.x * p.experts + e] = hist[e];
+    const float* column = reinterpret_cast<const float*>(sums) + e;
+    float v = column[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += column[w * kWide];
+    if (whole) {
+      p.counts[e] = hist[e];
+      p.grad[e] = (float)(share * hist[e]);
+      if (total > 0) loss += share * hist[e] * (double)v;
+    } else {
+      p.part_p[(int64_t)blockIdx.x * p.experts + e] = v;
+      p.part_c[(int64_t)blockIdx.x * p.experts + e] = hist[e];
+    }
   }
-  if (tid == 0) {
-    int total = 0;
-    for (int w = 0; w < W; ++w) total += counted[w];
-    p.part_n[blockIdx.x] = total;
+  if (!whole) {
+    if (tid == 0) p.part_n[blockIdx.x] = total;
+    return;
   }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) loss += __shfl_xor(loss, d);
+  __syncthreads();   // the columns are read
+  if (lane == 0) reinterpret_cast<double*>(sums)[wave] = loss;
+  __syncthreads();
+  if (wave) return;
+  if (lane == 0) {
+    for (int w = 1; w < W; ++w) loss += reinterpret_cast<double*>(sums)[w];
+    *p.loss = (float)loss;
+  }
+  write_offsets(p, lane, [&](int i) { return hist[i]; });
 }
 
-// Adds the workgroups' parts, in fp64 and in a fixed order, and writes what
-// follows from them.  One workgroup: Q groups of threads take every Q-th part.
+// Adds the workgroups' parts, in fp64 and in a fixed order: a workgroup those of
+// kJoin experts.  The last to be done (all of them count themselves) writes what
+// takes every expert: the loss and the offsets.
+constexpr int kJoin = 16;
 __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs p) {
-  __shared__ double dsum[1024];
-  __shared__ int isum[1024];
-  __shared__ int count[kMaxExperts];
-  const int tid = threadIdx.x;
-  int width = 1024;   // threads across the experts
-  while (width / 2 >= p.experts && width > 64) width /= 2;
-  const int q = tid / width, Q = 1024 / width;
-  int n = 0;
-  for (int b = tid; b < p.blocks; b += 1024) n += p.part_n[b];
-  isum[tid] = n;
-  __syncthreads();
-  for (int d = 512; d; d >>= 1) {
-    if (tid < d) isum[tid] += isum[tid + d];
-    __syncthreads();
-  }
-  const double tokens = (double)isum[0];
-  __syncthreads();
-  const double share = tokens > 0.0 ? (double)p.coef * p.experts / ((double)p.k * tokens * tokens) : 0.0;
-  double loss = 0.0;
-  for (int e0 = 0; e0 < p.experts; e0 += width) {   // one round where Q > 1
-    const int e = e0 + tid % width;
-    double s = 0.0;
-    int c = 0;
-    if (e < p.experts) {
-      for (int b = q; b < p.blocks; b += Q) {
-        s += (double)p.part_p[(int64_t)b * p.experts + e];
-        c += p.part_c[(int64_t)b * p.experts + e];
-      }
-    }
-    dsum[tid] = s;
-    isum[tid] = c;
-    __syncthreads();
-    if (q == 0 && e < p.experts) {
-      for (int o = 1; o < Q; ++o) {
-        s += dsum[tid + o * width];
-        c += isum[tid + o * width];
-      }
-      count[e] = c;
-      p.counts[e] = c;
-      p.grad[e] = (float)(share * c);
-      if (tokens > 0.0) loss += share * c * s;
+  __shared__ double dsum[16][kJoin];
+  __shared__ int isum[16][kJoin];
+  __shared__ bool last;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int e = blockIdx.x * kJoin + lane % kJoin;
+  int n = 0, c = 0;
+  double s = 0.0;
+  for (int b = lane; b < p.blocks; b += 64) n += p.part_n[b];   // every wave for itself
+  if (e < p.experts) {
+#pragma unroll 4
+    for (int b = wave * 4 + lane / kJoin; b < p.blocks; b += 64) {
+      s += (double)p.part_p[(int64_t)b * p.experts + e];
+      c += p.part_c[(int64_t)b * p.experts + e];
     }
   }
-  __syncthreads();
-  dsum[tid] = loss;
-  __syncthreads();
-  for (int d = 512; d; d >>= 1) {
-    if (tid < d) dsum[tid] += dsum[tid + d];
-    __syncthreads();
-  }
-  if (tid == 0) *p.loss = (float)dsum[0];
-  if (tid < 64) {   // sums of the counts before each expert
-    int64_t base = 0;
-    for (int e0 = 0; e0 < p.experts; e0 += 64) {
-      const int c = e0 + tid < p.experts ? count[e0 + tid] : 0;
-      int sum = c;
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(sum, d);
-        if (tid >= d) sum += v;
-      }
-      if (e0 + tid < p.experts) p.offsets[e0 + tid] = base + sum - c;
-      base += __builtin_amdgcn_readlane(sum, 63);
+  for (int d = 32; d; d >>= 1) {
+    n += __shfl_xor(n, d);
+    if (d >= kJoin) {
+      s += __shfl_xor(s, d);
+      c += __shfl_xor(c, d);
     }
-    if (tid == 0) p.offsets[p.experts] = base;
   }
+  if (lane < kJoin) {
+    dsum[wave][lane] = s;
+    isum[wave][lane] = c;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    const double share = n > 0 ? (double)p.coef * p.experts / ((double)p.k * n * n) : 0.0;
+    s = 0.0;
+    c = 0;
+    if (lane < kJoin) {
+#pragma unroll
+      for (int w = 0; w < 16; ++w) {
+        s += dsum[w][lane];
+        c += isum[w][lane];
+      }
+      if (e < p.experts) {
+        p.counts[e] = c;
+        p.grad[e] = (float)(share * c);
+      }
+    }
+    double loss = n > 0 ? share * c * s : 0.0;   // of nobody s may be anything, c is 0 past E
+#pragma unroll
+    for (int d = kJoin / 2; d; d >>= 1) loss += __shfl_xor(loss, d);
+    if (lane == 0) {
+      p.part_loss[blockIdx.x] = loss;
+      __threadfence();
+      last = atomicAdd(p.joined, 1u) + 1 == gridDim.x;
+    }
+  }
+  __syncthreads();
+  if (!last || wave) return;
+  __threadfence();
+  double loss = 0.0;
+  int64_t base = 0;
+  for (unsigned b = lane; b < gridDim.x; b += 64)
+    loss += __hip_atomic_load(&p.part_loss[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) loss += __shfl_xor(loss, d);
+  if (lane == 0) *p.loss = (float)loss;
+  write_offsets(p, lane, [&](int i) { return __hip_atomic_load(&p.counts[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); });
 }
 
 struct BalanceGradArgs {
@@ -279,20 +348,21 @@ __global__ __launch_bounds__(64 * W) void balance_grad_kernel(BalanceGradArgs p)
     f32x4 add[CH] = {};
     if (p.add) load_row<BF16, L, CH>(p.add, row, p.experts, l, 0.0f, add);
     if (row + step < p.tokens) load_row<BF16, L, CH>(p.x, row + step, p.experts, l, -INFINITY, next);
-    softmax_row<L, CH>(cur);
+    const float inv = softmax_row<L, CH>(cur);
     float dot = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
       for (int j = 0; j < 4; ++j) dot = fmaf(cur[c][j], v[c][j], dot);
-    dot = over_lanes<L>(dot, [](float a, float b) { return a + b; });
+    dot = over_lanes<L>(dot, [](float a, float b) { return a + b; }) * inv;
+    const float scale = dl * inv;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int e = 4 * (c * L + l);
       f32x4 d = add[c];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (in) d[j] += dl * cur[c][j] * (v[c][j] - dot);
+        if (in) d[j] = fmaf(scale * cur[c][j], v[c][j] - dot, d[j]);
       if (e + 4 <= p.experts) {
         store4<BF16>(p.out, row * p.experts + e, d);
       } else {
@@ -328,6 +398,8 @@ int balance_blocks(int64_t tokens, int experts) {
   return (int)(blocks < 1 ? 1 : (blocks < kBalanceBlocks ? blocks : kBalanceBlocks));
 }
 
+int64_t join_blocks(int experts) { return (experts + kJoin - 1) / kJoin; }
+
 }  // namespace
 }  // namespace fp4mi
 
@@ -335,7 +407,7 @@ using namespace fp4mi;
 
 extern "C" int64_t router_balance_workspace(int64_t tokens, int32_t num_experts) {
   if (tokens < 0 || tokens >= (int64_t(1) << 31) || num_experts < 1 || num_experts > kMaxExperts) return 0;
-  return (int64_t)balance_blocks(tokens, num_experts) * (8 * num_experts + 4);
+  return 16 + 8 * join_blocks(num_experts) + (int64_t)balance_blocks(tokens, num_experts) * (8 * num_experts + 4);
 }
 
 extern "C" int router_balance(const void* logits, int dtype, const void* experts, int index_size,
@@ -370,7 +442,10 @@ extern "C" int router_balance(const void* logits, int dtype, const void* experts
   }
   BalanceArgs p = {logits, experts, mask, tokens, slots, num_experts, k, coef, loss, counts, offsets, prob_grad};
   p.blocks = balance_blocks(tokens, num_experts);
-  p.part_p = static_cast<float*>(workspace);
+  const int64_t joins = join_blocks(num_experts);
+  p.joined = static_cast<uint32_t*>(workspace);
+  p.part_loss = reinterpret_cast<double*>(p.joined + 4);
+  p.part_p = reinterpret_cast<float*>(p.part_loss + joins);
   p.part_c = reinterpret_cast<int32_t*>(p.part_p + (int64_t)p.blocks * num_experts);
   p.part_n = p.part_c + (int64_t)p.blocks * num_experts;
   clear_stale_error();
@@ -382,7 +457,7 @@ extern "C" int router_balance(const void* logits, int dtype, const void* experts
                              : (wide ? balance_kernel<false, true, L, CH, W> : balance_kernel<false, false, L, CH, W>)),
                        dim3(p.blocks), dim3(64 * W), 0, st, p);
   });
-  hipLaunchKernelGGL(balance_join_kernel, dim3(1), dim3(1024), 0, st, p);
+  if (p.blocks > 1) hipLaunchKernelGGL(balance_join_kernel, dim3((unsigned)joins), dim3(1024), 0, st, p);
   return launch_status();
 }
 

@@ -1,4 +1,6 @@
 // SwiGLU into quantized rows with an 8-bit checkpoint, and its gradient.
+#include <string.h>
+
 #include "fp4mi_moe.h"
 #include "host_common.hpp"
 #include "rows_common.hpp"
@@ -6,26 +8,29 @@
 namespace fp4mi {
 namespace {
 
-// s = 1 / (1 + exp(-g)), 0 where exp(-g) is past fp32, and 1 - s: for g > 0 as
-// exp(-g) s, where the difference would lose what is left.
+// s = 1 / (1 + exp(-g)), 0 where exp(-g) is past fp32, and `rest` = 1 - s as exp(-g) s:
+// the difference would lose what is left for large g, and where s is 0 nothing takes
+// it.  BF16: exp(-g) with the argument rounded once, off by |g| 2^-24 of itself beside
+// its last places; what comes of it is rounded to 2^-9 or more.
+template <bool BF16>
 __device__ __forceinline__ float sigmoid(float g, float& rest) {
-  const float e = exp_f32(-g), s = __builtin_amdgcn_rcpf(1.0f + e);
-  rest = g > 0.0f ? e * s : 1.0f - s;
+  const float e = BF16 ? __builtin_amdgcn_exp2f(g * -0x1.715476p+0f) : exp_f32(-g);
+  const float s = __builtin_amdgcn_rcpf(1.0f + e);
+  rest = __uint_as_float(min(__float_as_uint(e), 0x7F7FFFFFu)) * s;   // not 0 times infinity
   return s;
 }
 
-// Row and octet of flat octet `i0 + local` of a tensor of d octets a row, from
-// those of i0; local < kSpan.  i0 is the workgroup's, so its 64-bit division is
-// scalar; magic = 2^32 / d rounded up is exact while (d + kSpan) d < 2^32, and a
-// longer row is passed at most once.
-constexpr int kSpan = 1024;
-struct OctetPlace {
+// Row and part of flat part `i0 + local` of a tensor of d parts a row, from those of
+// i0; local < kSpan.  i0 is the workgroup's, so its 64-bit division is scalar; magic =
+// 2^32 / d rounded up is exact while (d + kSpan) d < 2^32, and a longer row is passed at
+// most once.
+constexpr int kSpan = 512;   // parts a workgroup
+struct Place {
   int64_t row;
-  int oct;
+  int part;
 };
-__device__ __forceinline__ OctetPlace place_of(int64_t row0, uint32_t oct0, uint32_t local, uint32_t d,
-                                               uint32_t magic) {
-  const uint32_t o = oct0 + local;
+__device__ __forceinline__ Place place_of(int64_t row0, uint32_t part0, uint32_t local, uint32_t d, uint32_t magic) {
+  const uint32_t o = part0 + local;
   const uint32_t q = d >= kSpan ? (o >= d ? 1u : 0u) : __umulhi(o, magic);
   return {row0 + q, (int)(o - q * d)};
 }
@@ -37,109 +42,132 @@ struct SwigluArgs {
   void* q;
   void* scales;
   void* dx;
-  int64_t octets;       // rows * ffn / 8
-  uint32_t d, magic;    // ffn / 8
+  int64_t parts;        // of 16 bytes of dtype in rows * ffn
+  uint32_t d, magic;    // parts of ffn
 };
 
-// A thread takes an octet of y: the octets of g and u, of the same row.  Lanes
-// that share a block of y share blocks of g and u too.
+// A thread takes a part of y: those of g and u, of the same row.  Lanes that share
+// a block of y share blocks of g and u too.  Bound by memory: 65536 x 2048 bf16 with
+// the checkpoint 7.3 bytes a pair, 140 us (6.8 TB/s); the checkpoint is stored past the
+// caches, where it would push out y (170 us before), and the maxima of a block meet
+// as integers (each step one instruction).
 template <bool BF16, bool FP8>
 __global__ __launch_bounds__(kThreads) void swiglu_kernel(SwigluArgs p, int64_t blk0) {
-  constexpr int U = kSpan / kThreads / 2;
-  const int64_t i0 = ((int64_t)blockIdx.x + blk0) * (kThreads * U);
+  constexpr int U = kSpan / kThreads, V = Part<BF16>::kValues;
+  const int64_t i0 = ((int64_t)blockIdx.x + blk0) * kSpan;
   const int64_t row0 = i0 / p.d;
-  const uint32_t oct0 = (uint32_t)(i0 - row0 * p.d);
-  Octet<BF16> g[U], u[U];
+  const uint32_t part0 = (uint32_t)(i0 - row0 * p.d);
+  u32x4 g[U], u[U];
   int64_t at[U];
 #pragma unroll
   for (int c = 0; c < U; ++c) {
     const uint32_t local = c * kThreads + threadIdx.x;
-    const OctetPlace o = place_of(row0, oct0, local, p.d, p.magic);
-    at[c] = o.row * (2 * (int64_t)p.d) + o.oct;
-    if (i0 + local < p.octets) {
-      g[c] = octet_load<BF16>(p.x, at[c]);
-      u[c] = octet_load<BF16>(p.x, at[c] + p.d);
+    const Place o = place_of(row0, part0, local, p.d, p.magic);
+    at[c] = o.row * (2 * (int64_t)p.d) + o.part;
+    if (i0 + local < p.parts) {
+      g[c] = ld_u32x4(static_cast<const u32x4*>(p.x) + at[c]);
+      u[c] = ld_u32x4(static_cast<const u32x4*>(p.x) + at[c] + p.d);
     }
   }
 #pragma unroll
   for (int c = 0; c < U; ++c) {
     const int64_t i = i0 + c * kThreads + threadIdx.x;
-    if (i >= p.octets) continue;   // a block's lanes leave together
-    float gv[8], uv[8], y[8];
-    octet_values<BF16>(g[c], gv);
-    octet_values<BF16>(u[c], uv);
+    if (i >= p.parts) continue;   // a block's lanes leave together
+    float gv[V], uv[V], y[V];
+    part_values<BF16>(g[c], gv);
+    part_values<BF16>(u[c], uv);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < V; ++j) {
       float rest;
-      y[j] = gv[j] * sigmoid(gv[j], rest) * uv[j];
+      y[j] = gv[j] * sigmoid<BF16>(gv[j], rest) * uv[j];
     }
-    quantize_octet<FP8>(y, i, static_cast<uint8_t*>(p.q), p.scales);
+    quantize_part<FP8, false, V>(y, i, static_cast<uint8_t*>(p.q), p.scales);
     if (p.ckpt) {
-      quantize_octet<true>(gv, at[c], p.ckpt, p.ckpt_scales);
-      quantize_octet<true>(uv, at[c] + p.d, p.ckpt, p.ckpt_scales);
+      quantize_part<true, true, V>(gv, at[c], p.ckpt, p.ckpt_scales);
+      quantize_part<true, true, V>(uv, at[c] + p.d, p.ckpt, p.ckpt_scales);
     }
   }
 }
 
-// Octet of codes times its block's scale.
-__device__ __forceinline__ void kept_values(u32x2 c, float s, float (&v)[8]) {
+// V codes from part i of the checkpoint times their block's scale.
+template <int V>
+struct Kept {
+  uint32_t c[V / 4];
+  float s;
+};
+template <int V>
+__device__ __forceinline__ Kept<V> kept_load(const uint8_t* codes, const float* scales, int64_t i) {
+  Kept<V> k;
+  memcpy(k.c, __builtin_assume_aligned(codes + i * V, V), V);
+  k.s = scales[i / (128 / V)];
+  return k;
+}
+template <int V>
+__device__ __forceinline__ void kept_values(const Kept<V>& k, float (&v)[V]) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[h], false);
-    const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[h], true);
-    v[4 * h] = a.x * s;
-    v[4 * h + 1] = a.y * s;
-    v[4 * h + 2] = b.x * s;
-    v[4 * h + 3] = b.y * s;
+  for (int h = 0; h < V / 4; ++h) {
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)k.c[h], false);
+    const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)k.c[h], true);
+    v[4 * h] = a.x * k.s;
+    v[4 * h + 1] = a.y * k.s;
+    v[4 * h + 2] = b.x * k.s;
+    v[4 * h + 3] = b.y * k.s;
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void part_store(void* base, int64_t i, const float (&v)[Part<BF16>::kValues]) {
+  if constexpr (BF16) {
+    store8<true>(base, i, v);
+  } else {
+    st_u32x4(static_cast<u32x4*>(base) + i, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                                  __float_as_uint(v[2]), __float_as_uint(v[3])});
   }
 }
 
-// ROWS: 0 none, 1 MXFP4, 2 FP8.
+// ROWS: 0 none, 1 MXFP4, 2 FP8.  20011 x 2176 into bf16 54 us (6.5 TB/s); 65536 x 2048
+// into FP8 rows 128 us (6.4 TB/s, with the rows stored through the caches 140).
 template <bool BF16, int ROWS>
 __global__ __launch_bounds__(kThreads) void swiglu_grad_kernel(SwigluArgs p, int64_t blk0) {
-  constexpr int U = kSpan / kThreads / 2;
-  const int64_t i0 = ((int64_t)blockIdx.x + blk0) * (kThreads * U);
+  constexpr int U = kSpan / kThreads, V = Part<BF16>::kValues;
+  const int64_t i0 = ((int64_t)blockIdx.x + blk0) * kSpan;
   const int64_t row0 = i0 / p.d;
-  const uint32_t oct0 = (uint32_t)(i0 - row0 * p.d);
-  Octet<BF16> dy[U];
-  u32x2 g[U], u[U];
-  float gs[U], us[U];
+  const uint32_t part0 = (uint32_t)(i0 - row0 * p.d);
+  u32x4 dy[U];
+  Kept<V> g[U], u[U];
   int64_t at[U];
 #pragma unroll
   for (int c = 0; c < U; ++c) {
     const uint32_t local = c * kThreads + threadIdx.x;
-    const OctetPlace o = place_of(row0, oct0, local, p.d, p.magic);
-    at[c] = o.row * (2 * (int64_t)p.d) + o.oct;
-    if (i0 + local < p.octets) {
-      dy[c] = octet_load<BF16>(p.x, i0 + local);
-      g[c] = *reinterpret_cast<const u32x2*>(p.ckpt + 8 * at[c]);
-      u[c] = *reinterpret_cast<const u32x2*>(p.ckpt + 8 * (at[c] + p.d));
-      gs[c] = p.ckpt_scales[at[c] >> 4];
-      us[c] = p.ckpt_scales[(at[c] + p.d) >> 4];
+    const Place o = place_of(row0, part0, local, p.d, p.magic);
+    at[c] = o.row * (2 * (int64_t)p.d) + o.part;
+    if (i0 + local < p.parts) {
+      dy[c] = ld_u32x4(static_cast<const u32x4*>(p.x) + i0 + local);
+      g[c] = kept_load<V>(p.ckpt, p.ckpt_scales, at[c]);
+      u[c] = kept_load<V>(p.ckpt, p.ckpt_scales, at[c] + p.d);
     }
   }
 #pragma unroll
   for (int c = 0; c < U; ++c) {
     const int64_t i = i0 + c * kThreads + threadIdx.x;
-    if (i >= p.octets) continue;
-    float dv[8], gv[8], uv[8];
-    octet_values<BF16>(dy[c], dv);
-    kept_values(g[c], gs[c], gv);
-    kept_values(u[c], us[c], uv);
+    if (i >= p.parts) continue;
+    float dv[V], gv[V], uv[V];
+    part_values<BF16>(dy[c], dv);
+    kept_values<V>(g[c], gv);
+    kept_values<V>(u[c], uv);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < V; ++j) {
       float rest;
-      const float s = sigmoid(gv[j], rest), du = dv[j] * gv[j] * s;
-      gv[j] = dv[j] * uv[j] * s * fmaf(gv[j], rest, 1.0f);
+      const float d = dv[j] * sigmoid<BF16>(gv[j], rest), du = d * gv[j];
+      gv[j] = d * uv[j] * fmaf(gv[j], rest, 1.0f);
       uv[j] = du;
     }
     if (ROWS == 0 || p.dx) {
-      store8<BF16>(p.dx, at[c], gv);
-      store8<BF16>(p.dx, at[c] + p.d, uv);
+      part_store<BF16>(p.dx, at[c], gv);
+      part_store<BF16>(p.dx, at[c] + p.d, uv);
     }
     if constexpr (ROWS != 0) {
-      quantize_octet<ROWS == 2>(gv, at[c], static_cast<uint8_t*>(p.q), p.scales);
-      quantize_octet<ROWS == 2>(uv, at[c] + p.d, static_cast<uint8_t*>(p.q), p.scales);
+      quantize_part<ROWS == 2, true, V>(gv, at[c], static_cast<uint8_t*>(p.q), p.scales);
+      quantize_part<ROWS == 2, true, V>(uv, at[c] + p.d, static_cast<uint8_t*>(p.q), p.scales);
     }
   }
 }
@@ -159,12 +187,12 @@ bool any_overlap(const void* const* outs, const int64_t* outn, int no, const voi
   return false;
 }
 
-SwigluArgs swiglu_args(const void* x, int64_t rows, int64_t ffn) {
+SwigluArgs swiglu_args(const void* x, int isz, int64_t rows, int64_t ffn) {
   SwigluArgs p = {};
   p.x = x;
-  p.d = (uint32_t)(ffn / 8);
+  p.d = (uint32_t)(ffn * isz / 16);
   p.magic = (uint32_t)(((uint64_t(1) << 32) + p.d - 1) / p.d);
-  p.octets = rows * (ffn / 8);
+  p.parts = rows * p.d;
   return p;
 }
 
@@ -191,14 +219,14 @@ extern "C" int swiglu_quantize(const void* x, int dtype, int64_t rows, int64_t f
   const void* outs[4] = {q, scales, ckpt, ckpt_scales};
   const int64_t outn[4] = {code_bytes(n, fmt), scale_bytes(n), n2, scale_bytes(n2)}, inn = n2 * isz;
   if (any_overlap(outs, outn, 4, &x, &inn, 1)) return FP4_EOVERLAP;
-  SwigluArgs p = swiglu_args(x, rows, ffn);
+  SwigluArgs p = swiglu_args(x, isz, rows, ffn);
   p.q = q;
   p.scales = scales;
   p.ckpt = ckpt;
   p.ckpt_scales = ckpt_scales;
   clear_stale_error();
   hipStream_t st = as_stream(stream);
-  const int64_t blocks = (p.octets + kSpan / 2 - 1) / (kSpan / 2);
+  const int64_t blocks = (p.parts + kSpan - 1) / kSpan;
   const bool bf16 = dtype == FP4_DTYPE_BF16, fp8 = fmt == FP4_ROWS_FP8;
   launch_1d(bf16 ? (fp8 ? swiglu_kernel<true, true> : swiglu_kernel<true, false>)
                  : (fp8 ? swiglu_kernel<false, true> : swiglu_kernel<false, false>),
@@ -226,7 +254,7 @@ extern "C" int swiglu_backward(const void* dy, int dtype, const uint8_t* ckpt,
   const int64_t outn[3] = {n2 * isz, code_bytes(n2, fmt), scale_bytes(n2)};
   const int64_t inn[3] = {n * isz, n2, scale_bytes(n2)};
   if (any_overlap(outs, outn, 3, ins, inn, 3)) return FP4_EOVERLAP;
-  SwigluArgs p = swiglu_args(dy, rows, ffn);
+  SwigluArgs p = swiglu_args(dy, isz, rows, ffn);
   p.ckpt = const_cast<uint8_t*>(ckpt);
   p.ckpt_scales = const_cast<float*>(ckpt_scales);
   p.dx = dx;
@@ -234,7 +262,7 @@ extern "C" int swiglu_backward(const void* dy, int dtype, const uint8_t* ckpt,
   p.scales = scales;
   clear_stale_error();
   hipStream_t st = as_stream(stream);
-  const int64_t blocks = (p.octets + kSpan / 2 - 1) / (kSpan / 2);
+  const int64_t blocks = (p.parts + kSpan - 1) / kSpan;
   const bool bf16 = dtype == FP4_DTYPE_BF16;
   const int rows_fmt = !q ? 0 : (fmt == FP4_ROWS_FP8 ? 2 : 1);
   void (*kernels[2][3])(SwigluArgs, int64_t) = {

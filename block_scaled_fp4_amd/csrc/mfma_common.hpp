@@ -266,35 +266,35 @@ inline int64_t max_row_tiles(int64_t tokens, int64_t experts, int bm, bool group
 }
 
 // Four consecutive columns n .. n+3 of one output row, rounded once to the
-// output type (fp32 sums to here); columns past the row's end are dropped.
+// output type (fp32 sums to here); columns past the row's end are dropped.  A row
+// may begin at any element: whole vectors are stored at any alignment of it.
 template <bool BF16>
 __device__ __forceinline__ void store_out4(void* out, int64_t row, int n_cols, int n, f32x4 v) {
   if constexpr (BF16) {
     uint16_t* p = static_cast<uint16_t*>(out) + row * n_cols + n;
-    const uint32_t lo = pack_bf16x2(v.x, v.y), hi = pack_bf16x2(v.z, v.w);
-    if (n + 4 <= n_cols && (n_cols & 3) == 0) {
-      *reinterpret_cast<u32x2*>(p) = u32x2{lo, hi};
+    const u32x2 w = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+    if (n + 4 <= n_cols) {
+      __builtin_memcpy(p, &w, 8);
     } else {
-      if (n < n_cols) p[0] = (uint16_t)lo;
-      if (n + 1 < n_cols) p[1] = (uint16_t)(lo >> 16);
-      if (n + 2 < n_cols) p[2] = (uint16_t)hi;
-      if (n + 3 < n_cols) p[3] = (uint16_t)(hi >> 16);
+      if (n < n_cols) p[0] = (uint16_t)w.x;
+      if (n + 1 < n_cols) p[1] = (uint16_t)(w.x >> 16);
+      if (n + 2 < n_cols) p[2] = (uint16_t)w.y;
     }
   } else {
     float* p = static_cast<float*>(out) + row * n_cols + n;
-    if (n + 4 <= n_cols && (n_cols & 3) == 0) {
-      *reinterpret_cast<f32x4*>(p) = v;
+    if (n + 4 <= n_cols) {
+      __builtin_memcpy(p, &v, 16);
     } else {
       if (n < n_cols) p[0] = v.x;
       if (n + 1 < n_cols) p[1] = v.y;
       if (n + 2 < n_cols) p[2] = v.z;
-      if (n + 3 < n_cols) p[3] = v.w;
     }
   }
 }
 
 // 16 bytes at `src`: eight bf16 or four fp32 consecutive columns from n of one
-// output row; columns past the row's end are dropped.  Nontemporal: outputs of
+// output row, which may begin at any element; columns past its end are dropped (6061
+// tokens by 5668 x 768 in FP8: 72 us element by element).  Nontemporal: outputs of
 // whole tiles would push the operands out of the caches (plain stores against
 // these: the gradient of 16 x 4096 x 7168 1100 | 1072 us, 5001 tokens by 13 x
 // 7168 x 2048 170 | 159 us, 8192^3 in MXFP4 260 | 256 us).
@@ -303,8 +303,9 @@ __device__ __forceinline__ void store_chunk(void* out, int64_t row, int n_cols, 
                                             const uint8_t* src) {
   constexpr int kEl = BF16 ? 8 : 4;
   uint8_t* dst = static_cast<uint8_t*>(out) + (row * n_cols + n) * (16 / kEl);
-  if (n + kEl <= n_cols && n_cols % kEl == 0) {
-    st_u32x4(dst, *reinterpret_cast<const u32x4*>(src));
+  if (n + kEl <= n_cols) {
+    typedef u32x4 anywhere __attribute__((aligned(2)));
+    __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(src), reinterpret_cast<anywhere*>(dst));
   } else {
 #pragma unroll 1
     for (int j = 0; j < min(kEl, n_cols - n); ++j) {

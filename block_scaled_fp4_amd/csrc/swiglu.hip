@@ -21,18 +21,17 @@ __device__ __forceinline__ float sigmoid(float g, float& rest) {
 }
 
 // Row and part of flat part `i0 + local` of a tensor of d parts a row, from those of
-// i0; local < kSpan.  i0 is the workgroup's, so its 64-bit division is scalar; magic =
-// 2^32 / d rounded up is exact while (d + kSpan) d < 2^32, and a longer row is passed at
-// most once.
+// i0 (the workgroup's, so its 64-bit division is scalar); local < kSpan.  magic = 2^32
+// / d rounded up gives the quotient or, of operands below 2^20, one more.
 constexpr int kSpan = 512;   // parts a workgroup
 struct Place {
   int64_t row;
   int part;
 };
 __device__ __forceinline__ Place place_of(int64_t row0, uint32_t part0, uint32_t local, uint32_t d, uint32_t magic) {
-  const uint32_t o = part0 + local;
-  const uint32_t q = d >= kSpan ? (o >= d ? 1u : 0u) : __umulhi(o, magic);
-  return {row0 + q, (int)(o - q * d)};
+  const uint32_t o = part0 + local, q = __umulhi(o, magic);
+  const int part = (int)(o - q * d);
+  return {row0 + q - (part < 0 ? 1 : 0), part < 0 ? part + (int)d : part};
 }
 
 struct SwigluArgs {

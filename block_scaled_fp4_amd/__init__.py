@@ -121,7 +121,7 @@ def _stream_on(gpu, stream):
     one: a launch goes to the current GPU, whatever its pointers are."""
     if gpu != torch.cuda.current_device():
         raise ValueError(f"tensors are on GPU {gpu}, which is not the current one")
-    return _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(gpu) if stream is None else _stream(stream)
 
 
 def _on_stream(fn, args):

@@ -599,9 +599,12 @@ void launch_tiles(Fp8Args p, hipStream_t st) {
 // (16 tokens by 16384 x 4096 13.7, 64 x 32 14.9, 32 x 16 17.6; 64 tokens over 32
 // experts of 2048 x 4096 30.0, 33.5, 36.7), then 64 x 32 (256 tokens over the 32 46.8, 64 x
 // 64 51.8, tiles 43), 64 x 64 (1024 tokens 68.6, 64 x 32 72.9, tiles 76) and the tiles
-// (2048 tokens 87, 64 x 64 99).  With fp32 outputs the tiles take longer (512 tokens by
-// 4096 x 4096: 64 x 64 38, tiles 67, 1024 tokens 75 both; 4096 tokens over the 32: 191,
-// 273, 8192 tokens 349, 295).
+// (2048 tokens 87, 64 x 64 99).  Few experts leave the tiles few too, and 64 x 64 stays
+// ahead (448 tokens over 5 of 1393 x 3328: 264 workgroups 15.4, tiles 24.2; 2000 over 16
+// of 512 x 1024: 376 18.3, 11.4; dense 512 by 4096 x 4096: 512 25.8, 27.1, 1000 by 2000 x
+// 2048: 512 20.6, 16.4).  With fp32 outputs the tiles take longer (512 tokens by 4096 x
+// 4096: 64 x 64 38, tiles 67, 1024 tokens 75 both; 4096 tokens over the 32: 191, 273,
+// 8192 tokens 349, 295).
 template <bool BF16>
 void launch_product(const Fp8Args& p, hipStream_t st) {
   const int64_t per = p.tokens / p.experts;
@@ -614,7 +617,7 @@ void launch_product(const Fp8Args& p, hipStream_t st) {
   if (grouped ? per <= 4 : p.tokens <= 16) return launch_rows<4, 1, 4, 2, BF16>(p, st);
   if (count(32, 32) <= 256) return launch_rows<2, 2, 4, 4, BF16>(p, st);
   if (count(64, 32) <= 256 || (grouped && per <= 24)) return launch_rows<4, 2, 4, 2, BF16>(p, st);
-  if (grouped ? per <= (BF16 ? 40 : 160) : count(64, 64) <= (BF16 ? 384 : 1024))
+  if (count(64, 64) <= (BF16 ? (grouped ? 288 : 384) : 1024) || (grouped && per <= (BF16 ? 40 : 160)))
     return launch_rows<4, 4, 4, 2, BF16>(p, st);
   launch_tiles<BF16>(p, st);
 }

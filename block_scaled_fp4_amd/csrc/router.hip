@@ -147,8 +147,7 @@ __device__ __forceinline__ void write_offsets(const BalanceArgs& p, int lane, F 
 
 // A workgroup adds its rows' p in registers, row after row, its waves' sums in the
 // order of the waves, and leaves them, its counts and its number of counted tokens in
-// the workspace.  A call of one workgroup ends here (1 token of 256 experts 5.3 us, with
-// the second launch 11).
+// the workspace.  A call of one workgroup ends here.
 constexpr int kRowsAhead = 2;   // rows on their way
 template <bool BF16, bool IDX64, int L, int CH, int W>
 __global__ __launch_bounds__(64 * W) void balance_kernel(BalanceArgs p) {
@@ -389,11 +388,15 @@ void by_width(int experts, F f) {
 }
 
 constexpr int kBalanceBlocks = 256;
+// Rounds that one workgroup takes alone: the second launch costs the caller 3.5 us, and
+// eight rounds no more than two launches do on the card (512 tokens of 64 experts: 10.2
+// us, in two 9.2; a call with its allocations 14.4 us of the caller's time, in two 18).
+constexpr int kOneBlock = 8;
 int balance_blocks(int64_t tokens, int experts) {
   int64_t blocks = 0;
   by_width(experts, [&](auto l, auto, auto w) {
     constexpr int rows = 64 / decltype(l)::value * decltype(w)::value;
-    blocks = (tokens + rows - 1) / rows;
+    blocks = tokens <= kOneBlock * rows ? 1 : (tokens + rows - 1) / rows;
   });
   return (int)(blocks < 1 ? 1 : (blocks < kBalanceBlocks ? blocks : kBalanceBlocks));
 }

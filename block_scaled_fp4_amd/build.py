@@ -2,10 +2,12 @@
 
 Usage: python block_scaled_fp4_amd/build.py   (or call build()).
 """
+import concurrent.futures
 import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -15,7 +17,7 @@ SOURCES = ["quant.hip", "fp4quant.hip", "fp8col.hip", "matmul.hip", "wgrad.hip",
            "fp8quant.hip", "fp8mat.hip", "swiglu.hip", "router.hip", "abi.hip"]
 
 FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-fno-gpu-flush-denormals-to-zero", "-fhip-fp32-correctly-rounded-divide-sqrt",
     "-ffp-contract=off",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -31,17 +33,28 @@ def hipcc():
 
 
 def build(verbose=False):
+    """Every source to an object of its own, side by side, then one library."""
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), *FLAGS, "-I", os.path.join(ROOT, "include"),
-           *[os.path.join(CSRC, s) for s in SOURCES], "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
+    with tempfile.TemporaryDirectory() as out, concurrent.futures.ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objects = [os.path.join(out, s + ".o") for s in SOURCES]
+        common = [hipcc(), *FLAGS]
+        cmds = [[*common, "-c", "-I", os.path.join(ROOT, "include"), os.path.join(CSRC, s), "-o", o]
+                for s, o in zip(SOURCES, objects)]
+        done = list(pool.map(lambda c: _run(c, verbose), cmds))
+        done.append(_run([*common, "-shared", *objects, "-o", tmp], verbose) if all(done) else False)
+    if not all(done):
         raise RuntimeError("hipcc failed building libfp4mi.so")
     os.replace(tmp, LIB)
     return LIB
+
+
+def _run(cmd, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode:
+        sys.stderr.write(r.stdout + r.stderr)
+    return r.returncode == 0
 
 
 if __name__ == "__main__":

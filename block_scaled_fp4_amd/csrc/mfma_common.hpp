@@ -13,7 +13,7 @@
 #include <type_traits>
 #include <utility>
 
-#include "device_common.hpp"
+#include "lane_common.hpp"
 
 namespace fp4mi {
 

@@ -2,7 +2,7 @@
 // maxima over lanes, and the codes and scales of a block.
 #pragma once
 
-#include "device_common.hpp"
+#include "lane_common.hpp"
 
 namespace fp4mi {
 

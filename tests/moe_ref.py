@@ -5,6 +5,7 @@ below 2^-6.  Where the value that is rounded went through fp32 operations, `slac
 is their relative error, which moves a value across a boundary at most by itself.
 """
 import numpy as np
+import torch
 
 from ops_ref import U
 from oracle import formats as F
@@ -71,9 +72,9 @@ def product_bounds(a, b, row, bf16):
     c, mag = a @ b.T, np.abs(a) @ np.abs(b).T
     bound = (a.shape[1] + 16) * (U * mag + 2.0 ** -126)
     if bf16:
-        x, y = np.abs(a).reshape(a.shape[0], -1, 8), np.abs(b).reshape(b.shape[0], -1, 8)
+        x, y = (torch.from_numpy(np.ascontiguousarray(np.abs(v))).view(v.shape[0], -1, 8) for v in (a, b))
         for i in range(a.shape[0]):
-            bound[i] += 7 * 2.0 ** -13 * (x[i][None] * y).max(-1).sum(-1)
+            bound[i] += 7 * 2.0 ** -13 * (x[i] * y).amax(-1).sum(-1).numpy()
     if row is not None:
         r = row.astype(np.float64)[:, None]
         c, bound = c * r, bound * np.abs(r)

@@ -41,7 +41,8 @@ def run(m, a, sa, w, sw, row, bf16, off=None):
 
 # few rows, then tiles: sides around each tile's, lengths around each stage
 SHAPES = [(1, 1, 128), (1, 130, 256), (3, 16, 1152), (16, 33, 384), (17, 65, 640), (77, 1001, 2176), (130, 260, 128),
-          (257, 5000, 384), (600, 2311, 256), (255, 8200, 1024), (513, 4097, 640), (1300, 1284, 896)]
+          (257, 5000, 384), (600, 2311, 256), (255, 8200, 1024), (513, 4097, 640), (1300, 1284, 896),
+          (1100, 4100, 128), (1100, 4101, 256), (1027, 4102, 384)]
 
 
 @pytest.mark.parametrize("bf16", [True, False])
@@ -60,7 +61,8 @@ def test_dense(m, n, k, tile, bf16):
 @pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("counts,n,k", [
     ([1], 128, 128), ([3, 0, 1, 2], 200, 384), ([0, 0, 5], 64, 256), ([40, 0, 100, 1, 60], 300, 512),
-    ([300, 0, 129, 1], 700, 640), ([256, 512, 0, 255, 257], 513, 384), ([1000, 24], 260, 1152)])
+    ([300, 0, 129, 1], 700, 640), ([256, 512, 0, 255, 257], 513, 384), ([1000, 24], 260, 1152),
+    ([700, 0, 90, 513], 3001, 384), ([60, 0, 75, 41] * 33, 300, 128), ([200, 300, 0, 129, 1, 256] * 12, 200, 256)])
 def test_grouped(counts, n, k, bf16):
     mod = need_gpu()
     rng = np.random.default_rng(sum(counts) + n)
@@ -80,7 +82,7 @@ def test_grouped(counts, n, k, bf16):
 
 
 @pytest.mark.parametrize("bf16", [True, False])
-@pytest.mark.parametrize("m,n", [(5, 40), (700, 2500)])
+@pytest.mark.parametrize("m,n", [(5, 40), (700, 2500), (1100, 4100)])
 def test_far_scales_and_nan(m, n, bf16):
     """Scales at both ends of their range beside blocks of zeros, and NaN codes and
     scales, which reach the outputs that read them and no others."""
@@ -159,16 +161,19 @@ def test_malformed_offsets_stay_inside():
     """Clamped on the device: rows outside every shard are not written."""
     mod = need_gpu()
     rng = np.random.default_rng(3)
-    for T, n in ((20, 64), (400, 600)):
+    for T, n in ((20, 64), (400, 600), (1400, 4200)):
         a, sa = R.random_fp8(rng, T, 256)
         ws = [weights(rng, n, 256, True) for _ in range(3)]
         for off in ([-5, 3, 2, T + 9], [0, T, T, T - 4], [4, 6, 9, 11]):
-            out = Guarded(T * n * 4)
-            mod.fp8_matmul_grouped(dev_u8(a), dev_f32(sa), dev_u8(np.stack([w[0] for w in ws])),
-                                   dev_f32(np.stack([w[1] for w in ws])), dev_i64(np.array(off)),
-                                   out=out.view(torch.float32, (T, n)))
-            torch.cuda.synchronize()
-            out.check()
+            for dt, size in ((torch.float32, 4), (torch.bfloat16, 2)):
+                out = Guarded(T * n * size)
+                v = out.view(dt, (T, n))
+                mod.fp8_matmul_grouped(dev_u8(a), dev_f32(sa), dev_u8(np.stack([w[0] for w in ws])),
+                                       dev_f32(np.stack([w[1] for w in ws])), dev_i64(np.array(off)), out=v)
+                torch.cuda.synchronize()
+                out.check()
+                if off[0] == 4:                      # rows before the first shard keep what they held
+                    assert bool((v[:4].view(torch.uint8) == 0xA5).all())
 
 
 def test_float8_views_and_leading_shapes():

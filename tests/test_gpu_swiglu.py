@@ -36,7 +36,7 @@ def row_bufs(rows, width, fmt):
 
 @pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("fmt", ["fp8", "mxfp4"])
-@pytest.mark.parametrize("rows,ffn", [(1, 128), (1, 2048), (3, 8192), (5, 384), (33, 640), (300, 256), (17, 8320)])
+@pytest.mark.parametrize("rows,ffn", [(1, 128), (1, 2048), (3, 8192), (5, 384), (33, 640), (300, 256), (17, 8320), (2, 393344)])
 def test_forward(rows, ffn, fmt, bf16):
     m = need_gpu()
     x, v = inputs(np.random.default_rng(rows + ffn), rows, ffn, bf16)
@@ -71,7 +71,7 @@ def kept(rng, rows, ffn):
 
 @pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("fmt", [None, "fp8", "mxfp4"])
-@pytest.mark.parametrize("rows,ffn", [(1, 128), (1, 2048), (3, 8192), (5, 384), (33, 640), (300, 256), (17, 8320)])
+@pytest.mark.parametrize("rows,ffn", [(1, 128), (1, 2048), (3, 8192), (5, 384), (33, 640), (300, 256), (17, 8320), (2, 393344)])
 def test_backward(rows, ffn, fmt, bf16):
     m = need_gpu()
     rng = np.random.default_rng(rows * ffn)

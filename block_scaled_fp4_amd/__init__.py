@@ -602,15 +602,15 @@ def fp8_quantize(x, q=None, scales=None, stream=None):
     shape, gpu = x.shape, x.get_device()
     cols = shape[-1]
     rows = x.numel() // cols if cols else 0
-    n = rows * cols
+    n, new = rows * cols, q is None and scales is None
     if q is None:
         q = torch.empty_like(x, dtype=torch.uint8)
     else:
         q = _codes(q)
     if scales is None:
         scales = x.new_empty((*shape[:-1], cols // 128), dtype=torch.float32)
-    if not (gpu >= 0 and _fits(x, x.dtype, n, gpu) and _fits(q, torch.uint8, n, gpu)
-            and _fits(scales, torch.float32, n // 128, gpu)):
+    if not (gpu >= 0 and _fits(x, x.dtype, n, gpu)
+            and (new or (_fits(q, torch.uint8, n, gpu) and _fits(scales, torch.float32, n // 128, gpu)))):
         _dev(x)
         _arg(q, "q", torch.uint8, n, x.device)
         _arg(scales, "scales", torch.float32, n // 128, x.device)
@@ -669,12 +669,13 @@ def _fp8_product(name, a, a_scales, a_row_scale, w, w_scales, offsets, out_dtype
     srows = w_scales.shape[-2] if w_scales.dim() > 1 else -1
     if srows not in (N, (N + 127) // 128):
         raise ValueError(f"the weights' scales must have {N} rows or {(N + 127) // 128} rows of blocks")
-    if out is None:
+    new = out is None
+    if new:
         out = a.new_empty((M, N) if len(shape) == 2 else (*shape[:-1], N), dtype=out_dtype)
     ns, nws = M * (K // 128), E * srows * (K // 128)
     if not (gpu >= 0 and _fits(a, torch.uint8, M * K, gpu) and _fits(a_scales, torch.float32, ns, gpu)
             and _fits(w, torch.uint8, E * N * K, gpu) and _fits(w_scales, torch.float32, nws, gpu)
-            and _fits(out, out.dtype, M * N, gpu)
+            and (new or _fits(out, out.dtype, M * N, gpu))
             and (a_row_scale is None or _fits(a_row_scale, torch.float32, M, gpu))
             and (offsets is None or _fits(offsets, torch.int64, E + 1, gpu))):
         _dev(a)
@@ -749,22 +750,22 @@ def swiglu_quantize(x, fmt="fp8", checkpoint=True, q=None, scales=None, ckpt=Non
     rows = x.numel() // width if width else 0
     fp8 = fmt == "fp8"
     per, block, sdt = (1, 128, torch.float32) if fp8 else (2, 32, torch.uint8)
+    new = q is None and scales is None and ckpt is None and ckpt_scales is None
     if q is None:
         q = x.new_empty((*lead, ffn // per), dtype=torch.uint8)
+    else:
+        q = _codes(q)
     if scales is None:
         scales = x.new_empty((*lead, ffn // block), dtype=sdt)
-    if checkpoint and ckpt is None:
-        ckpt = torch.empty_like(x, dtype=torch.uint8)
-    if checkpoint and ckpt_scales is None:
-        ckpt_scales = x.new_empty((*lead, width // 128), dtype=torch.float32)
-    q = _codes(q)
-    n = rows * ffn
     if checkpoint:
-        ckpt = _codes(ckpt)
-    if not (gpu >= 0 and _fits(x, dt, 2 * n, gpu) and _fits(q, torch.uint8, n // per, gpu)
-            and _fits(scales, sdt, n // block, gpu)
-            and (not checkpoint or (_fits(ckpt, torch.uint8, 2 * n, gpu)
-                                    and _fits(ckpt_scales, torch.float32, n // 64, gpu)))):
+        ckpt = torch.empty_like(x, dtype=torch.uint8) if ckpt is None else _codes(ckpt)
+        if ckpt_scales is None:
+            ckpt_scales = x.new_empty((*lead, width // 128), dtype=torch.float32)
+    n = rows * ffn
+    if not (gpu >= 0 and _fits(x, dt, 2 * n, gpu)
+            and (new or (_fits(q, torch.uint8, n // per, gpu) and _fits(scales, sdt, n // block, gpu)
+                         and (not checkpoint or (_fits(ckpt, torch.uint8, 2 * n, gpu)
+                                                 and _fits(ckpt_scales, torch.float32, n // 64, gpu)))))):
         _dev(x)
         _arg(q, "q", torch.uint8, n // per, x.device)
         _arg(scales, "scales", sdt, n // block, x.device)
@@ -842,6 +843,7 @@ def router_balance(logits, experts, coef=1.0, mask=None, loss=None, counts=None,
     size = 4 if experts.dtype is torch.int32 else 8
     idt = torch.int32 if size == 4 else torch.int64
     need = _lib.router_balance_workspace(tokens, E)
+    new = loss is None and counts is None and offsets is None and prob_grad is None and workspace is None
     if loss is None:
         loss = logits.new_empty(1, dtype=torch.float32)
     if counts is None:
@@ -853,9 +855,10 @@ def router_balance(logits, experts, coef=1.0, mask=None, loss=None, counts=None,
     if workspace is None:
         workspace = logits.new_empty(need, dtype=torch.uint8)
     if not (gpu >= 0 and _fits(logits, dt, tokens * E, gpu) and _fits(experts, idt, tokens * k, gpu)
-            and (mask is None or _fits(mask, torch.uint8, tokens, gpu)) and _fits(loss, torch.float32, 1, gpu)
-            and _fits(counts, torch.int32, E, gpu) and _fits(offsets, torch.int64, E + 1, gpu)
-            and _fits(prob_grad, torch.float32, E, gpu) and _fits(workspace, torch.uint8, need, gpu)):
+            and (mask is None or _fits(mask, torch.uint8, tokens, gpu))
+            and (new or (_fits(loss, torch.float32, 1, gpu) and _fits(counts, torch.int32, E, gpu)
+                         and _fits(offsets, torch.int64, E + 1, gpu) and _fits(prob_grad, torch.float32, E, gpu)
+                         and _fits(workspace, torch.uint8, need, gpu)))):
         _dev(logits)
         _arg(experts, "experts", idt, tokens * k, logits.device)
         _arg(mask, "mask", torch.uint8, tokens, logits.device, optional=True)
@@ -887,12 +890,13 @@ def router_balance_backward(logits, prob_grad, dloss=None, mask=None, add=None, 
     mask = _mask_bytes(mask)
     gpu, dt, n, E = logits.get_device(), logits.dtype, logits.numel(), logits.shape[-1]
     tokens = n // E if E else 0
-    if dlogits is None:
+    new = dlogits is None
+    if new:
         dlogits = torch.empty_like(logits)
     if not (gpu >= 0 and _fits(logits, dt, n, gpu) and _fits(prob_grad, torch.float32, E, gpu)
             and (dloss is None or _fits(dloss, torch.float32, 1, gpu))
             and (mask is None or _fits(mask, torch.uint8, tokens, gpu))
-            and (add is None or _fits(add, dt, n, gpu)) and _fits(dlogits, dt, n, gpu)):
+            and (add is None or _fits(add, dt, n, gpu)) and (new or _fits(dlogits, dt, n, gpu))):
         _dev(logits)
         _arg(prob_grad, "prob_grad", torch.float32, E, logits.device)
         _arg(dloss, "dloss", torch.float32, 1, logits.device, optional=True)

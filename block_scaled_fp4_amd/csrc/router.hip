@@ -83,9 +83,11 @@ __device__ __forceinline__ float over_lanes(float v, F f) {
 }
 
 // exp(x - max) of a row in place; returns the factor that makes them its softmax.  The
-// maximum is taken times log2(e), rounded: that moves all of a row alike, and x - max
-// is rounded once, in the fma.  A row of -inf alone becomes zeros; NaN and +inf make
-// the factor NaN.
+// maximum is taken times log2(e), rounded: that moves all of a row alike, by 2^-4 at
+// most for a maximum below 2^20, and x - max is rounded once, in the fma.  Past that
+// (rows filled with a type's lowest value: the product would be infinite) the maximum
+// is subtracted first.  A row of -inf alone becomes zeros; NaN and +inf make the
+// factor NaN.
 template <int L, int CH>
 __device__ __forceinline__ float softmax_row(f32x4 (&v)[CH]) {
   float top = -INFINITY;
@@ -93,7 +95,15 @@ __device__ __forceinline__ float softmax_row(f32x4 (&v)[CH]) {
   for (int c = 0; c < CH; ++c) top = fmaxf(fmaxf(fmaxf(v[c].x, v[c].y), fmaxf(v[c].z, v[c].w)), top);
   top = over_lanes<L>(top, [](float a, float b) { return fmaxf(a, b); });
   constexpr float kLog2e = 0x1.715476p+0f;
-  const float m = top == -INFINITY ? 0.0f : top * kLog2e;
+  float m = top * kLog2e;
+  if (!(fabsf(top) < 0x1p20f)) {
+    const float from = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[c][j] -= from;
+    m = 0.0f;
+  }
   float sum = 0.0f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {

@@ -162,6 +162,54 @@ def test_nan_and_infinity_in_counted_rows():
         assert torch.isfinite(loss).item() and torch.isfinite(m.router_balance_backward(x, v, mask=mask)).all()
 
 
+def huge_rows(dt, e):
+    """Rows of masks and values far past any exponent, with p known exactly: even over
+    the places of the largest value."""
+    low, rows, top = torch.finfo(dt).min, [], []
+
+    def add(base, places, value):
+        r = torch.full((e,), base, dtype=dt)
+        r[places] = value
+        rows.append(r)
+        top.append(r == r.max())
+
+    for base in (low, -1e30, -3e9, 3e9, 1e30, torch.finfo(dt).max):   # one value throughout
+        add(base, [], 0.0)
+    for base in (low, -1e30, -3e9):                                   # a few places left
+        add(base, [0, e - 1], 2.5)
+        add(base, [1], 0.0)
+    add(-float("inf"), [0, 2], low)
+    add(-float("inf"), [2], 3e9)
+    add(low, [1, 2], torch.finfo(dt).max)
+    return torch.stack(rows), torch.stack(top).double() / torch.stack(top).sum(-1, keepdim=True)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e", [3, 8, 61, 100, 256, 400, 1000, 1500])
+def test_masks_of_the_lowest_value_and_huge_logits(e, dt):
+    """A place of p is 1 / n, off by the exponential, the sum and the division, as p_tol
+    with x = max; every other place lies
+    10^9 or more below the largest, and its p is 0."""
+    m = need_gpu()
+    x, p = huge_rows(dt, e)
+    t = x.shape[0]
+    idx = np.random.default_rng(e).integers(0, e, (t, 2))
+    c = np.bincount(idx.reshape(-1), minlength=e)
+    v = 0.5 * e * c / (2.0 * t * t)
+    loss, counts, _, grad = m.router_balance(x.cuda(), torch.from_numpy(idx).cuda(), 0.5)
+    np.testing.assert_array_equal(host(counts), c)
+    want = float((v * p.numpy().sum(0)).sum())
+    assert abs(float(loss) - want) <= U * (16 + 64) * want, (float(loss), want)
+    got = m.router_balance_backward(x.cuda(), grad).double().cpu().numpy()
+    v = host(grad).astype(np.float64)
+    p = p.numpy()
+    dot = (p * v).sum(-1, keepdims=True)
+    ref = p * (v - dot)
+    half = 2.0 ** -8 if dt == torch.bfloat16 else 2.0 ** -24
+    tol = 4 * U * 32 * p * (v + dot) + 1e-38 + half * np.abs(ref) * 1.01
+    assert (np.abs(got - ref) <= tol).all(), np.argwhere(~(np.abs(got - ref) <= tol))[:4].tolist()
+
+
 def test_unaligned_rows_and_repeatability():
     """Rows that begin at any element, and the same bits from call to call."""
     m = need_gpu()

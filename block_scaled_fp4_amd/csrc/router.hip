@@ -383,7 +383,9 @@ __global__ __launch_bounds__(64 * W) void balance_grad_kernel(BalanceGradArgs p)
 }
 
 // Lanes of a row and its chunks a lane: the fewest lanes that hold it in one
-// chunk, then more chunks.  f(integral constants L, CH, W).
+// chunk, then more chunks.  Places past a row's end cost what the others do: 20000 x
+// 1500 fp32 in 8 chunks 43 us and its gradient 69, in 16 80 and 160.
+// f(integral constants L, CH, W).
 template <int N>
 using Int = std::integral_constant<int, N>;
 template <typename F>
@@ -394,6 +396,7 @@ void by_width(int experts, F f) {
   else if (experts <= 256) f(Int<64>(), Int<1>(), Int<16>());
   else if (experts <= 512) f(Int<64>(), Int<2>(), Int<16>());
   else if (experts <= 1024) f(Int<64>(), Int<4>(), Int<8>());
+  else if (experts <= 2048) f(Int<64>(), Int<8>(), Int<8>());
   else f(Int<64>(), Int<16>(), Int<4>());
 }
 

@@ -156,9 +156,8 @@ int swiglu_backward(const void* dy, int dtype, const uint8_t* ckpt, const float*
  *               (workspace_bytes; FP4_ESHAPE if fewer), 16-byte aligned.  Sums are
  *               added in a fixed order: results do not vary between calls
  * A logit of -inf has p = 0, a row of nothing else has p = 0 throughout, one filled
- * with the lowest finite value 1 / E; NaN or
- * +inf in a counted row makes the loss NaN.  No output may overlap an input,
- * the workspace or another output.
+ * with the lowest finite value 1 / E; NaN or +inf in a counted row makes the loss
+ * NaN.  No output may overlap an input, the workspace or another output.
  */
 int router_balance(const void* logits, int dtype, const void* experts, int index_size,
                    const uint8_t* mask, int64_t tokens, int32_t num_experts, int32_t k, float coef,

@@ -42,7 +42,8 @@ def dev_mask(mask):
 
 SIZES = [(1, 1, 1), (1, 8, 2), (2, 3, 3), (7, 33, 4), (100, 61, 8), (513, 64, 1), (300, 130, 6), (1000, 256, 8),
          (77, 257, 2), (50, 511, 8), (40, 1000, 3), (9, 1025, 2), (11, 4096, 2), (20000, 16, 2),
-         (700, 100, 3), (200, 400, 2), (150, 1000, 3), (100, 3000, 4), (3000, 5, 40)]
+         (700, 100, 3), (200, 400, 2), (150, 1000, 3), (100, 3000, 4), (3000, 5, 40),
+         (300, 1100, 3), (70, 2048, 2), (70, 2049, 2)]
 
 
 @pytest.mark.parametrize("bf16", [True, False])

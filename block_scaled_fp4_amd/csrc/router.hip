@@ -83,11 +83,9 @@ __device__ __forceinline__ float over_lanes(float v, F f) {
 }
 
 // exp(x - max) of a row in place; returns the factor that makes them its softmax.  The
-// maximum is taken times log2(e), rounded: that moves all of a row alike, by 2^-4 at
-// most for a maximum below 2^20, and x - max is rounded once, in the fma.  Past that
-// (rows filled with a type's lowest value: the product would be infinite) the maximum
-// is subtracted first.  A row of -inf alone becomes zeros; NaN and +inf make the
-// factor NaN.
+// maximum is subtracted before log2(e) is multiplied in: times it, a type's lowest
+// value is infinite, and a maximum past 2^30 is rounded by more than the exponent
+// holds.  A row of -inf alone becomes zeros; NaN and +inf make the factor NaN.
 template <int L, int CH>
 __device__ __forceinline__ float softmax_row(f32x4 (&v)[CH]) {
   float top = -INFINITY;
@@ -95,21 +93,13 @@ __device__ __forceinline__ float softmax_row(f32x4 (&v)[CH]) {
   for (int c = 0; c < CH; ++c) top = fmaxf(fmaxf(fmaxf(v[c].x, v[c].y), fmaxf(v[c].z, v[c].w)), top);
   top = over_lanes<L>(top, [](float a, float b) { return fmaxf(a, b); });
   constexpr float kLog2e = 0x1.715476p+0f;
-  float m = top * kLog2e;
-  if (!(fabsf(top) < 0x1p20f)) {
-    const float from = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[c][j] -= from;
-    m = 0.0f;
-  }
+  const float from = top == -INFINITY ? 0.0f : top;
   float sum = 0.0f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[c][j] = __builtin_amdgcn_exp2f(fmaf(v[c][j], kLog2e, -m));
+      v[c][j] = __builtin_amdgcn_exp2f((v[c][j] - from) * kLog2e);
       sum += v[c][j];
     }
   }
@@ -391,7 +381,7 @@ __global__ __launch_bounds__(64 * W) void balance_grad_kernel(BalanceGradArgs p)
 
 // Lanes of a row and its chunks a lane: the fewest lanes that hold it in one
 // chunk, then more chunks.  Places past a row's end cost what the others do: 20000 x
-// 1500 fp32 in 8 chunks 43 us and its gradient 69, in 16 80 and 160.
+// 1500 fp32 in 8 chunks 45 us and its gradient 69, in 16 80 and 160.
 // f(integral constants L, CH, W).
 template <int N>
 using Int = std::integral_constant<int, N>;

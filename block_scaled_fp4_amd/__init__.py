@@ -41,6 +41,7 @@ FMT = {"nvfp4": 0, "mxfp4": 1}
 ROUND = {"rtn": 0, "sr": 1}
 TSCALE = {"compute": 0, "given": 1}
 ROWS = {"mxfp4": 0, "fp8": 1}
+EXACT = 0x100   # or'ed to the output type of the products of FP8 by FP8
 
 _p, _i, _i32, _i64, _u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
 _f = ctypes.c_float
@@ -658,7 +659,7 @@ def fp8_quantize_blocks(x, transposed=False, q=None, scales=None, q_t=None, scal
     return q, scales, q_t, scales_t
 
 
-def _fp8_product(name, a, a_scales, a_row_scale, w, w_scales, offsets, out_dtype, out, stream):
+def _fp8_product(name, a, a_scales, a_row_scale, w, w_scales, offsets, out_dtype, out, stream, exact):
     """Checks and launches either product of FP8 by FP8."""
     a, w = _codes(a), _codes(w)
     shape, gpu = a.shape, a.get_device()
@@ -687,39 +688,40 @@ def _fp8_product(name, a, a_scales, a_row_scale, w, w_scales, offsets, out_dtype
         _arg(a_row_scale, "a_row_scale", torch.float32, M, a.device, optional=True)
         _arg(offsets, "token_offsets", torch.int64, E + 1, a.device, optional=True)
     row = None if a_row_scale is None else a_row_scale.data_ptr()
-    block = 1 if srows == N else 128
+    block, code = 1 if srows == N else 128, _dtype_code(out.dtype) | (EXACT if exact else 0)
     if offsets is None:
         status = _lib.fp8_matmul(a.data_ptr(), a_scales.data_ptr(), row, w.data_ptr(), w_scales.data_ptr(),
-                                 block, M, N, K, out.data_ptr(), _dtype_code(out.dtype), _stream_on(gpu, stream))
+                                 block, M, N, K, out.data_ptr(), code, _stream_on(gpu, stream))
     else:
         status = _lib.fp8_matmul_grouped(a.data_ptr(), a_scales.data_ptr(), row, w.data_ptr(),
                                          w_scales.data_ptr(), block, offsets.data_ptr(), E, M, N, K,
-                                         out.data_ptr(), _dtype_code(out.dtype), _stream_on(gpu, stream))
+                                         out.data_ptr(), code, _stream_on(gpu, stream))
     _check(name, status)
     return out
 
 
 def fp8_matmul(a, a_scales, b, b_scales, a_row_scale=None, out_dtype=torch.bfloat16, out=None,
-               stream=None):
+               stream=None, exact=False):
     """a [.., K] . b [N, K]^T -> [.., N] in out_dtype (or out's dtype).
 
     a in FP8 rows (E4M3, uint8 or float8_e4m3fn, with power-of-two fp32 scales
     [.., K/128]), b with scales [N, K/128] (FP8 rows) or [ceil(N/128), K/128] (FP8
-    blocks).  a_row_scale: fp32 factor per row of a.  fp32 outputs are sums of
-    exact products; for bf16 outputs products far below their neighbours along K
-    are dropped (2e-5 of a sum of Gaussian values)."""
+    blocks).  a_row_scale: fp32 factor per row of a.  fp32 outputs are fp32 sums of
+    exact products.  bf16 outputs are that with exact=True; without it, of every 8
+    products along K, what lies below 2^-13 of the largest is dropped (2e-5 of a sum
+    of Gaussian values), which takes 0.4 to 1.0 of the time."""
     if stream is not None and out is None:
         return _on_stream(fp8_matmul, locals())
     if b.dim() != 2:
         raise ValueError("b must be [N, K]")
-    return _fp8_product("fp8_matmul", a, a_scales, a_row_scale, b, b_scales, None, out_dtype, out, stream)
+    return _fp8_product("fp8_matmul", a, a_scales, a_row_scale, b, b_scales, None, out_dtype, out, stream, exact)
 
 
 def fp8_matmul_grouped(a, a_scales, w, w_scales, token_offsets, a_row_scale=None,
-                       out_dtype=torch.bfloat16, out=None, stream=None):
+                       out_dtype=torch.bfloat16, out=None, stream=None, exact=False):
     """Rows token_offsets[e] .. token_offsets[e+1]-1 of a [T, K] times w[e]^T,
     w [E, N, K] with scales [E, N, K/128] or [E, ceil(N/128), K/128] -> [T, N].
-    Operands as fp8_matmul."""
+    Operands, and exact, as fp8_matmul."""
     if stream is not None and out is None:
         return _on_stream(fp8_matmul_grouped, locals())
     if w.dim() != 3 or w_scales.dim() != 3:
@@ -727,7 +729,7 @@ def fp8_matmul_grouped(a, a_scales, w, w_scales, token_offsets, a_row_scale=None
     if token_offsets is None:
         raise ValueError("token_offsets is required")
     return _fp8_product("fp8_matmul_grouped", a, a_scales, a_row_scale, w, w_scales, token_offsets,
-                        out_dtype, out, stream)
+                        out_dtype, out, stream, exact)
 
 
 def swiglu_quantize(x, fmt="fp8", checkpoint=True, q=None, scales=None, ckpt=None, ckpt_scales=None,

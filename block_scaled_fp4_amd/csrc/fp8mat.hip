@@ -99,7 +99,10 @@ __device__ __forceinline__ i32x8 words(const Frag<true>& f) {
 // cache a look-up: 64 tokens by 4096 x 4096 12.1 us so, 8.6 by way of LDS, 256 tokens
 // 42.6 and 13.4.)  Bound by memory where the weights are large: 64 tokens over 32
 // experts of 2048 x 7168 48 us, 5.5 TB/s; one token by 4096 x 7168 5.3 us.
-template <int FN, int FM, int W, int NB, bool BF16>
+// EXACT: products of bf16 values, added in fp32, in place of the scaled instruction,
+// which drops the lowest bits of 8 products that it adds together.  One token 5.9 us,
+// 64 over the 32 experts 47.8 for 47.3, 256 by 4096 x 4096 19.2 for 13.0.
+template <int FN, int FM, int W, int NB, bool BF16, bool EXACT>
 __global__ __launch_bounds__(64 * W) void fp8_rows_product_kernel(Fp8Args p, int64_t blk0) {
   static_assert(8 % NB == 0, "eight steps end where they began");
   constexpr int kLoads = 2 * (FN + FM), kStep = 16 * (FN + FM) * 128;
@@ -186,7 +189,7 @@ __global__ __launch_bounds__(64 * W) void fp8_rows_product_kernel(Fp8Args p, int
       __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): read, and free for the next
       __builtin_amdgcn_wave_barrier();
       fetch(B, c + S + NB);
-      if constexpr (BF16) {
+      if constexpr (!EXACT) {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -222,11 +225,11 @@ __global__ __launch_bounds__(64 * W) void fp8_rows_product_kernel(Fp8Args p, int
   }
 }
 
-template <int FN, int FM, int W, int NB, bool BF16>
+template <int FN, int FM, int W, int NB, bool BF16, bool EXACT>
 void launch_rows(Fp8Args p, hipStream_t st) {
   p.n_tiles = (p.n + 16 * FN - 1) / (16 * FN);
   const int64_t blocks = p.n_tiles * max_row_tiles(p.tokens, p.experts, 16 * FM, p.offsets != nullptr);
-  launch_1d(fp8_rows_product_kernel<FN, FM, W, NB, BF16>, blocks, 64 * W, st, p);
+  launch_1d(fp8_rows_product_kernel<FN, FM, W, NB, BF16, EXACT>, blocks, 64 * W, st, p);
 }
 
 // ------------------------------------------------------------- many rows
@@ -287,6 +290,7 @@ __device__ __forceinline__ void load_step(const uint8_t* row, const float* scale
 // 128 columns by `rows` tokens of a tile, 16 x 16 at a time straight from memory, for
 // scales of any range.  Out of line, like the above, so that it costs the common
 // path no registers.
+template <bool BF16>
 __device__ __attribute__((noinline)) void rare_quarter(Fp8View v, int mw, int rows, int nw, void* out,
                                                        int64_t out_row, int n_cols, const float* row_scale) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -304,7 +308,7 @@ __device__ __attribute__((noinline)) void rare_quarter(Fp8View v, int mw, int ro
     }
     if (m + r < v.xrows) {
       if (row_scale) c[0][0] *= row_scale[out_row + m + r];
-      store_out4<false>(out, out_row + m + r, n_cols, v.n0 + n + 4 * g, c[0][0]);
+      store_out4<BF16>(out, out_row + m + r, n_cols, v.n0 + n + 4 * g, c[0][0]);
     }
   }
 }
@@ -326,11 +330,12 @@ __device__ __attribute__((noinline)) void rare_quarter(Fp8View v, int mw, int ro
 // (428), as the touch is waited for in its turn.  Where weights come from memory a
 // stage waits for them (16384 tokens, 512 each for 32 experts of 4096 x 7168 420 us, the
 // same product with one weight 343).
-// For fp32 outputs (BF16 false) four 32 x 32 x 16 products of bf16 values, which hold
-// code times scale exactly, take the place of a scaled one.  Their time is that of
+// Exact products (EXACT: fp32 outputs, or bf16 ones where the caller asks for them) are
+// four 32 x 32 x 16 products of bf16 values, which hold code times scale exactly, in
+// the place of a scaled one.  Their time is that of
 // the products (twice the scaled one's) and of the conversions, which do not run
 // beside them (16 cycles each, as many for two products as one takes; spread evenly
-// between the products they cost the same): 8192^3 1021 us.
+// between the products they cost the same): 8192^3 1018 us, into bf16 1000.
 template <int FM>
 struct Fp8TileShared {
   static constexpr int kBuffers = FM == 4 ? 2 : 3, kStage = (256 + 64 * FM) * 128;
@@ -349,7 +354,7 @@ union Fp8TileMemory {
   Fp8TileShared<FM> t;
   uint8_t out[4][quarter_bytes<4, BF16>()];
 };
-template <int FM, bool BF16>
+template <int FM, bool BF16, bool EXACT>
 __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM, BF16>& sh, int e, int row0, int row_end,
                                          int nt) {
   constexpr int FN = 4, BM = 64 * FM, kAll = FN * FM, kLoads = 2 * (FN + FM);
@@ -393,7 +398,7 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM, BF1
     const int past = min(max(s - max(stages - 4, 0), 0), 3);   // stages past the end get any scale
     const auto pack = [&](u32x4& v) {
       asm volatile("" : "+v"(v));   // else each is loaded as its upper half alone
-      if constexpr (!BF16) {
+      if constexpr (EXACT) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) odd |= !scale_in_window((int)(v[j] >> 23 & 0xFFu));
       }
@@ -472,7 +477,7 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM, BF1
     xsc = xsn;
     unrolled<2 * kAll>([&](auto idx) {
       constexpr int i = decltype(idx)::value, ks = i / kAll, j = i % kAll;
-      if constexpr (BF16) {
+      if constexpr (!EXACT) {
         constexpr int I = j / FM, J = j % FM;
         acc[I][J] = mfma_fp8<I, J>(step[ks].w[I], step[ks].x[J], acc[I][J], wsc, xsc);
       } else {
@@ -546,7 +551,7 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM, BF1
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) read(0, 0, i, step[0]);
   read_scales(0);
-  if constexpr (!BF16) {
+  if constexpr (EXACT) {
 #pragma unroll
     for (int f = 0; f < FM; ++f) to_y(std::integral_constant<int, 0>(), f, step[0], xsn);
     to_v(std::integral_constant<int, 0>(), step[0], wsn);
@@ -560,11 +565,11 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM, BF1
   }
   __builtin_amdgcn_s_waitcnt(0x0070);   // what was asked for past the end has landed too
   __syncthreads();
-  if constexpr (!BF16) {
+  if constexpr (EXACT) {
     const Fp8View view = {x, w, p.a_scales + (int64_t)row0 * stages,
                           p.w_scales + (int64_t)e * p.scale_rows * stages, p.k, min(xrows, BM), wrows, n0, p.scale_shift};
     if (__syncthreads_or(odd) && __syncthreads_or(scales_need_care<BM>(view))) {
-      rare_quarter(view, wm * 32 * FM, 32 * FM, wn * 128, p.out, row0, p.n, p.a_row_scale);
+      rare_quarter<BF16>(view, wm * 32 * FM, 32 * FM, wn * 128, p.out, row0, p.n, p.a_row_scale);
       return;
     }
   }
@@ -572,7 +577,7 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& p, Fp8TileMemory<FM, BF1
                               p.a_row_scale);
 }
 
-template <bool BF16>
+template <bool BF16, bool EXACT>
 __global__ __launch_bounds__(256, 1) void fp8_tiles_kernel(Fp8Args p, int64_t blk0) {
   __shared__ __align__(16) union {
     Fp8TileMemory<4, BF16> whole;
@@ -582,18 +587,18 @@ __global__ __launch_bounds__(256, 1) void fp8_tiles_kernel(Fp8Args p, int64_t bl
   bool half;
   place_tile(p, (int64_t)blockIdx.x + blk0, mt, nt);
   if (!locate_mixed(p, mt, e, row0, row_end, half)) return;
-  if (half) fp8_tile<2, BF16>(p, sh.half, e, row0, row_end, nt);
-  else fp8_tile<4, BF16>(p, sh.whole, e, row0, row_end, nt);
+  if (half) fp8_tile<2, BF16, EXACT>(p, sh.half, e, row0, row_end, nt);
+  else fp8_tile<4, BF16, EXACT>(p, sh.whole, e, row0, row_end, nt);
 }
 
-template <bool BF16>
+template <bool BF16, bool EXACT>
 void launch_tiles(Fp8Args p, hipStream_t st) {
   const bool grouped = p.offsets != nullptr;
   p.n_tiles = (p.n + 255) / 256;
   p.m_tiles = max_row_tiles(p.tokens, p.experts, 256, grouped);
   p.tall = p.m_tiles * p.n_tiles > 192;
   if (!p.tall) p.m_tiles = max_row_tiles(p.tokens, p.experts, 128, grouped);
-  launch_1d(fp8_tiles_kernel<BF16>, p.n_tiles * p.m_tiles, 256, st, p);
+  launch_1d(fp8_tiles_kernel<BF16, EXACT>, p.n_tiles * p.m_tiles, 256, st, p);
 }
 
 // Which kernel.  A few-row kernel's time hardly changes while each of its workgroups
@@ -610,24 +615,24 @@ void launch_tiles(Fp8Args p, hipStream_t st) {
 // (2048 tokens 87, 64 x 64 99).  Few experts leave the tiles few too, and 64 x 64 stays
 // ahead (448 tokens over 5 of 1393 x 3328: 264 workgroups 15.4, tiles 24.2; 2000 over 16
 // of 512 x 1024: 376 18.3, 11.4; dense 512 by 4096 x 4096: 512 25.8, 27.1, 1000 by 2000 x
-// 2048: 512 20.6, 16.4).  With fp32 outputs the tiles take longer (512 tokens by 4096 x
-// 4096: 64 x 64 38, tiles 67, 1024 tokens 75 both; 4096 tokens over the 32: 191, 273,
-// 8192 tokens 349, 295).
-template <bool BF16>
+// 2048: 512 20.6, 16.4).  With exact products the tiles take longer (fp32 outputs: 512
+// tokens by 4096 x 4096: 64 x 64 38, tiles 67, 1024 tokens 75 both; 4096 tokens over the
+// 32: 191, 273, 8192 tokens 349, 295).
+template <bool BF16, bool EXACT>
 void launch_product(const Fp8Args& p, hipStream_t st) {
   const int64_t per = p.tokens / p.experts;
   const bool grouped = p.offsets != nullptr;
   auto count = [&](int cols, int rows) {
     return (int64_t)((p.n + cols - 1) / cols) * max_row_tiles(p.tokens, p.experts, rows, grouped);
   };
-  if (count(16, 16) <= 256) return launch_rows<1, 1, 8, 2, BF16>(p, st);
-  if (count(32, 16) <= 256) return launch_rows<2, 1, 8, 2, BF16>(p, st);
-  if (grouped ? per <= 4 : p.tokens <= 16) return launch_rows<4, 1, 4, 2, BF16>(p, st);
-  if (count(32, 32) <= 256) return launch_rows<2, 2, 4, 4, BF16>(p, st);
-  if (count(64, 32) <= 256 || (grouped && per <= 24)) return launch_rows<4, 2, 4, 2, BF16>(p, st);
-  if (count(64, 64) <= (BF16 ? (grouped ? 288 : 384) : 1024) || (grouped && per <= (BF16 ? 40 : 160)))
-    return launch_rows<4, 4, 4, 2, BF16>(p, st);
-  launch_tiles<BF16>(p, st);
+  if (count(16, 16) <= 256) return launch_rows<1, 1, 8, 2, BF16, EXACT>(p, st);
+  if (count(32, 16) <= 256) return launch_rows<2, 1, 8, 2, BF16, EXACT>(p, st);
+  if (grouped ? per <= 4 : p.tokens <= 16) return launch_rows<4, 1, 4, 2, BF16, EXACT>(p, st);
+  if (count(32, 32) <= 256) return launch_rows<2, 2, 4, 4, BF16, EXACT>(p, st);
+  if (count(64, 32) <= 256 || (grouped && per <= 24)) return launch_rows<4, 2, 4, 2, BF16, EXACT>(p, st);
+  if (count(64, 64) <= (EXACT ? 1024 : (grouped ? 288 : 384)) || (grouped && per <= (EXACT ? 160 : 40)))
+    return launch_rows<4, 4, 4, 2, BF16, EXACT>(p, st);
+  launch_tiles<BF16, EXACT>(p, st);
 }
 
 // Checks shared by both products; experts == 0 stands for the plain one.
@@ -635,6 +640,8 @@ int product(const uint8_t* a, const float* a_scales, const float* a_row_scale, c
             const float* w_scales, int block_rows, const int64_t* offsets, int32_t experts, int64_t T,
             int64_t N, int64_t K, void* out, int out_dtype, void* stream) {
   if (block_rows != 1 && block_rows != 128) return FP4_EINVAL;
+  const bool exact = (out_dtype & FP4_EXACT) != 0;
+  out_dtype &= ~FP4_EXACT;
   const int osz = dtype_size(out_dtype);
   if (!osz) return FP4_EDTYPE;
   const int64_t E = experts ? experts : 1;
@@ -660,8 +667,9 @@ int product(const uint8_t* a, const float* a_scales, const float* a_row_scale, c
   Fp8Args p = {a, a_scales, a_row_scale, w, w_scales, offsets, out, T, (int)E, (int)N, (int)K,
                block_rows == 1 ? 0 : 7, (int)scale_rows, 0, 0, false};
   clear_stale_error();
-  if (out_dtype == FP4_DTYPE_BF16) launch_product<true>(p, as_stream(stream));
-  else launch_product<false>(p, as_stream(stream));
+  if (out_dtype == FP4_DTYPE_F32) launch_product<false, true>(p, as_stream(stream));
+  else if (exact) launch_product<true, true>(p, as_stream(stream));
+  else launch_product<true, false>(p, as_stream(stream));
   return launch_status();
 }
 

@@ -48,9 +48,11 @@ __device__ __forceinline__ f32x4 mfma_scaled(const Frag<false>& a, const Frag<fa
 // Gaussian rows), which is not a sum in fp32.  E2M1 by E2M1 spans 8 bits within
 // a block and loses nothing, whatever the other blocks' scales are (of a block
 // that cancels 2^0 to 2^40 above its neighbour the rest is 0.2 of fp32's last
-// place at most).  But E4M3 goes through bf16 products, which are exact and are
-// added in fp32 (6e-8 measured), at half the scaled instruction's rate.  A
-// lane then holds the 32 consecutive k from 32 g of both operands, and
+// place at most).  E4M3 goes through bf16 products, which are exact and are
+// added in fp32 (6e-8 measured), at half the scaled instruction's rate: with
+// MXFP4 weights, in the weight gradient, and of FP8 by FP8 wherever the output is
+// fp32 or the caller asks for exact products; other bf16 outputs of FP8 by FP8
+// take the scaled instruction, as their entry points state.  A lane then holds the 32 consecutive k from 32 g of both operands, and
 // instruction q of four takes its 8 from 8 q.
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 

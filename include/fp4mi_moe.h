@@ -115,7 +115,8 @@ int fp8_matmul_grouped(const uint8_t* a, const float* a_scales, const float* a_r
  *               without a checkpoint)
  *  fmt          FP4_ROWS_MXFP4 or FP4_ROWS_FP8
  *  q, scales    out: rows of y, [rows, ffn] in the layout of fmt; 16- and 4-byte
- *               aligned.  y is computed in fp32 from x itself
+ *               aligned.  y is computed in fp32 from x itself, within 2^-20 of
+ *               itself (0 where g is below -87: exp(-g) leaves fp32's range)
  *  ckpt         out E4M3 [rows, 2 ffn], 16-byte aligned, or NULL (inference)
  *  ckpt_scales  out fp32 [rows, 2 ffn/128], 4-byte aligned; NULL with ckpt
  * Outputs must not overlap x or each other.
@@ -125,7 +126,8 @@ int swiglu_quantize(const void* x, int dtype, int64_t rows, int64_t ffn, int fmt
 
 /*
  * swiglu_backward -- gradient of silu(g) * u at the checkpoint's g and u:
- *   dx = [dy u s (1 + g (1 - s)) | dy g s],  s = 1 / (1 + exp(-g)).
+ *   dx = [dy u s (1 + g (1 - s)) | dy g s],  s = 1 / (1 + exp(-g)),
+ * in fp32, within 2^-20 of the terms' size before it is rounded.
  *
  *  dy           [rows, ffn] in dtype, 16-byte aligned
  *  ckpt, ckpt_scales   as swiglu_quantize wrote them

@@ -164,7 +164,9 @@ int swiglu_backward(const void* dy, int dtype, const uint8_t* ckpt, const float*
  *               backward pass.  Zeros, like the loss, where n is 0
  *  workspace    scratch of router_balance_workspace(tokens, E) bytes or more
  *               (workspace_bytes; FP4_ESHAPE if fewer), 16-byte aligned.  Sums are
- *               added in a fixed order: results do not vary between calls
+ *               added in a fixed order: results do not vary between calls.  p is
+ *               added in fp32 over 128 rows at most, one after another, then over
+ *               a workgroup's such sums; the workgroups' in fp64
  * A logit of -inf has p = 0, a row of nothing else has p = 0 throughout, one filled
  * with the lowest finite value 1 / E; NaN or +inf in a counted row makes the loss
  * NaN.  No output may overlap an input, the workspace or another output.

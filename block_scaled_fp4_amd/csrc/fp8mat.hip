@@ -133,7 +133,9 @@ __global__ __launch_bounds__(64 * W) void fp8_rows_product_kernel(Fp8Args p, int
     for (int i = 0; i < kLoads; ++i)
       load_to_lds(i < 2 * FN ? wb : xb, off[i], (uint32_t)min(c, steps - 1) * 128, &sh.rows[wave][b][i * 1024]);
   };
-  // The scales of eight steps of each fragment's row, as bytes.
+  // The scales of eight steps of each fragment's row, as bytes.  The compiler loads the upper
+  // half of each word by itself, fragment after fragment, and waits for all there is
+  // in flight: FN + FM times every eight steps.
   const float *ws[FN], *xs[FM];
 #pragma unroll
   for (int f = 0; f < FN; ++f)
@@ -323,7 +325,7 @@ __device__ __attribute__((noinline)) void rare_quarter(Fp8View v, int mw, int ro
 // buffer.
 // A row's eight 16-byte chunks lie at position chunk ^ (row / 2 % 8): 16 rows of a
 // fragment read take every bank once.
-// 8192^3 in 382 to 397 us, 2.8 PFLOP/s: the matrix cores are busy 73% of the cycles, at
+// 8192^3 in 381 to 422 us from card to card, 2.6 to 2.9 PFLOP/s: the matrix cores are busy 73% of the cycles, at
 // the 1.8 GHz that the card holds under this load; with loads and reads left out the
 // products take 280.  Half blocks of k in four buffers, requests of 64 bytes and twice
 // the barriers, took 431; touching the lines of later stages ahead made it slower
@@ -332,10 +334,11 @@ __device__ __attribute__((noinline)) void rare_quarter(Fp8View v, int mw, int ro
 // same product with one weight 343).
 // Exact products (EXACT: fp32 outputs, or bf16 ones where the caller asks for them) are
 // four 32 x 32 x 16 products of bf16 values, which hold code times scale exactly, in
-// the place of a scaled one.  Their time is that of
-// the products (twice the scaled one's) and of the conversions, which do not run
-// beside them (16 cycles each, as many for two products as one takes; spread evenly
-// between the products they cost the same): 8192^3 1018 us, into bf16 1000.
+// the place of a scaled one.  Their time is that of the products (twice the scaled
+// one's) and of the conversions, which do not run beside them (16 cycles each, as many
+// for two products as one takes; spread evenly between the products they cost the
+// same): 8192^3 1018 to 1033 us, into bf16 1000.  32 and 48 vector registers are spilled
+// there, behind the stages' loop and ahead of the output.
 template <int FM>
 struct Fp8TileShared {
   static constexpr int kBuffers = FM == 4 ? 2 : 3, kStage = (256 + 64 * FM) * 128;
@@ -617,7 +620,9 @@ void launch_tiles(Fp8Args p, hipStream_t st) {
 // of 512 x 1024: 376 18.3, 11.4; dense 512 by 4096 x 4096: 512 25.8, 27.1, 1000 by 2000 x
 // 2048: 512 20.6, 16.4).  With exact products the tiles take longer (fp32 outputs: 512
 // tokens by 4096 x 4096: 64 x 64 38, tiles 67, 1024 tokens 75 both; 4096 tokens over the
-// 32: 191, 273, 8192 tokens 349, 295).
+// 32: 191, 273, 8192 tokens 349, 295).  The average is all that the host knows: where one shard of
+// many experts has all the tokens, its weights are read once for each 16 to 64 of them
+// (4096 tokens of 1024 experts of 512 x 1024 142 us, spread evenly 240, as one product 12).
 template <bool BF16, bool EXACT>
 void launch_product(const Fp8Args& p, hipStream_t st) {
   const int64_t per = p.tokens / p.experts;

@@ -87,6 +87,10 @@ __device__ __forceinline__ float over_lanes(float v, F f) {
 // maximum is subtracted before log2(e) is multiplied in: times it, a type's lowest
 // value is infinite, and a maximum past 2^30 is rounded by more than the exponent
 // holds.  A row of -inf alone becomes zeros; NaN and +inf make the factor NaN.
+// exp2's argument is rounded once more than the difference x - max itself, and as much
+// (half of fp32's last place each), so p is off by 2.1e-7 (relative, root mean
+// square) where exp of the difference gives 1.6e-7; exp_f32 in its place took 65536 x 256
+// from 26 to 29 us, its gradient in bf16 from 22 to 25.
 template <int L, int CH>
 __device__ __forceinline__ float softmax_row(f32x4 (&v)[CH]) {
   float top = -INFINITY;
@@ -149,7 +153,10 @@ __device__ __forceinline__ void write_offsets(const BalanceArgs& p, int lane, F 
 // A workgroup adds its rows' p in registers, row after row, its waves' sums in the
 // order of the waves, and leaves them, its counts and its number of counted tokens in
 // the workspace.  A call of one workgroup ends here.
-constexpr int kRowsAhead = 2;   // rows on their way
+// The rows asked for ahead are on their way in fp32.  bf16 is unpacked inside load_row's
+// branch, which waits for each load there: 65536 x 256 28 us, in fp32 26; 20000 x 2500 133
+// and 89.
+constexpr int kRowsAhead = 2;
 template <bool BF16, bool IDX64, int L, int CH, int W>
 __global__ __launch_bounds__(64 * W) void balance_kernel(BalanceArgs p) {
   constexpr int R = 64 / L, kWide = L * CH * 4;   // rows a wave takes at once, columns
@@ -335,8 +342,10 @@ template <bool BF16, int L, int CH, int W>
 __global__ __launch_bounds__(64 * W) void balance_grad_kernel(BalanceGradArgs p) {
   constexpr int R = 64 / L;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (L - 1), sub = lane / L;
-  // The next row is on its way, but for 16 chunks, where registers run out (20000 rows
-  // of 2500: bf16 152 us, 282 with it, fp32 116, 161; of 4096: 214, 379 and 184, 173).
+  // The next row is asked for ahead but where a lane has 16 chunks, on the measurement alone
+  // (20000 rows of 2500: bf16 154 us, 282 with it, fp32 117, 161; of 4096: 216, 379 and 184,
+  // 173; no registers are spilled either way).  bf16 rows, of half the bytes, take longer than
+  // fp32 there: load_row unpacks them in its branch and so waits for chunk after chunk.
   constexpr bool kAhead = CH <= 8;
   f32x4 v[CH], cur[CH], next[CH];
   load_row<false, L, CH>(p.v, 0, p.experts, l, 0.0f, v);
@@ -399,8 +408,8 @@ void by_width(int experts, F f) {
 }
 
 constexpr int kBalanceBlocks = 256;
-// Rounds that one workgroup takes alone: the second launch costs the caller 3.5 us, and
-// eight rounds no more than two launches do on the card (512 tokens of 64 experts: 10.2
+// Rounds that one workgroup takes alone: eight take about 1 us more on the card than two
+// launches do, and the second launch costs the caller 3.5 us (512 tokens of 64 experts: 10.2
 // us, in two 9.2; a call with its allocations 14.4 us of the caller's time, in two 18).
 constexpr int kOneBlock = 8;
 // Rows that a lane adds up in fp32; the workgroups' sums are added in fp64.  Rows alike,

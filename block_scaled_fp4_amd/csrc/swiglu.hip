@@ -58,7 +58,7 @@ struct SwigluArgs {
 
 // A thread takes a part of y: those of g and u, of the same row.  Lanes that share
 // a block of y share blocks of g and u too.  Bound by memory: 65536 x 2048 bf16 with
-// the checkpoint 7.3 bytes a pair, 140 us (6.8 TB/s); the checkpoint is stored past the
+// the checkpoint 7.1 bytes a pair, 140 us (6.8 TB/s); the checkpoint is stored past the
 // caches, where it would push out y (170 us before), and the maxima of a block meet
 // as integers (each step one instruction).
 template <bool BF16, bool FP8>

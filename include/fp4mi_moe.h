@@ -81,8 +81,8 @@ int fp8_quantize_blocks(const void* x, int dtype, int64_t batch, int64_t rows, i
  * at most 7 * 2^-13 of each run's largest product: 2e-5 of a sum of Gaussian values,
  * where bf16 itself rounds by up to 2^-8, but all of a sum whose large products cancel
  * and leave small ones of the same runs.  FP4_EXACT takes 1.0 to 1.2 times as long for
- * up to 64 rows, 2.6 times for thousands (4096 x 4096 by 1, 256, 2048 rows: 5.1 us for
- * 4.6, 19 for 13, 75 for 35).
+ * up to 64 rows, 2.1 to 2.6 times for thousands (4096 x 4096 by 1, 256, 2048 rows: 5.1 us
+ * for 4.6, 19 for 13, 75 for 35).
  * A NaN code, or an exponent field of 255 in a scale, makes the outputs that read it
  * NaN.
  */

@@ -168,7 +168,7 @@ def operands(mod):
     return a, sa, w, sw, dev_i64(np.array([0, 1900, 3585]))
 
 
-def calls(mod, stream=None):
+def calls(mod):
     a, sa, w, sw, off = operands(mod)
     for dt in (BF, F32):
         yield lambda dt=dt, **kw: mod.fp8_matmul(a, sa, w[0], sw[0], out_dtype=dt, **kw)
